@@ -19,7 +19,10 @@ LIB_PATH = os.environ.get("BQM_LIB") or os.path.join(_HERE, "libbqm.so")
 
 Q4_0 = 2
 Q8_0 = 8
-FMT = {"q4_0": Q4_0, "q8_0": Q8_0}
+MXFP4 = 39
+FMT = {"q4_0": Q4_0, "q8_0": Q8_0, "mxfp4": MXFP4}
+TYPE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 30}  # bqm_type
+SCORE = {"softmax": 0, "sigmoid": 1}
 QMV_MAX_M = 8
 QMV_ID_MAX_T = 64
 QMM_ID_MAX_T = 16384
@@ -63,6 +66,15 @@ def lib():
         L.bqm_chain_prepare.argtypes = [P, I, P, P]
         L.qmv_chain.argtypes = [I, I, P, I, P]
         L.bqm_chain_status.argtypes = [P, P]
+        L.bqm_quantize_mxfp4.argtypes = [I, P, I64, P, I64, I64, P]
+        L.bqm_dequantize_mxfp4.argtypes = [P, I, P, I64, I64, I64, P]
+        L.qmv_mxfp4.argtypes = [P, P, P, I, I64, I64, P]
+        L.qmm_mxfp4.argtypes = [P, P, P, I64, I64, I64, P]
+        L.qmm_id_mxfp4.argtypes = [P, I, I64, I64, P, I, I, P, I64, I64, I64, P, P]
+        L.bqm_route.argtypes = [I, I, P, I64, P, I, I, I, I, I, I, I, ctypes.c_float, P, P, P]
+        for f in ("bqm_quantize_mxfp4", "bqm_dequantize_mxfp4", "qmv_mxfp4", "qmm_mxfp4", "qmm_id_mxfp4",
+                  "bqm_route"):
+            getattr(L, f).restype = I
         for f in ("bqm_chain_prepare", "qmv_chain", "bqm_chain_status"):
             getattr(L, f).restype = I
         L.bqm_strerror.argtypes = [I]
@@ -163,6 +175,41 @@ def qmm_id(fmt, w_packed, E: int, N: int, K: int, ids, T: int, top_k: int, Xq, d
            x_tok_rows: int, x_slot_rows: int, Y, stream=None):
     _call("qmm_id", _fmt(fmt), _ptr(w_packed), E, N, K, _ptr(ids), T, top_k, _ptr(Xq), _ptr(dx),
           x_tok_rows, x_slot_rows, _ptr(Y), _stream(stream))
+
+
+def _type(t):
+    return TYPE.get(t.dtype, -1)  # the library refuses an unknown type
+
+
+def bqm_quantize_mxfp4(X, x_stride: int, packed, rows: int, K: int, stream=None):
+    """Rows of fp32, fp16 or bf16 (by X's dtype), x_stride elements apart -> packed MXFP4."""
+    _call("bqm_quantize_mxfp4", _type(X), _ptr(X), x_stride, _ptr(packed), rows, K, _stream(stream))
+
+
+def bqm_dequantize_mxfp4(packed, Y, y_stride: int, rows: int, K: int, stream=None):
+    """Packed MXFP4 -> rows of Y's dtype, y_stride elements apart."""
+    _call("bqm_dequantize_mxfp4", _ptr(packed), _type(Y), _ptr(Y), y_stride, rows, K, _stream(stream))
+
+
+def qmv_mxfp4(w_packed, X, Y, M: int, N: int, K: int, stream=None):
+    _call("qmv_mxfp4", _ptr(w_packed), _ptr(X), _ptr(Y), M, N, K, _stream(stream))
+
+
+def qmm_mxfp4(w_packed, x_packed, Y, M: int, N: int, K: int, stream=None):
+    _call("qmm_mxfp4", _ptr(w_packed), _ptr(x_packed), _ptr(Y), M, N, K, _stream(stream))
+
+
+def qmm_id_mxfp4(w_packed, E: int, N: int, K: int, ids, T: int, top_k: int, x_packed, x_rows: int,
+                 x_tok_rows: int, x_slot_rows: int, Y, stream=None):
+    _call("qmm_id_mxfp4", _ptr(w_packed), E, N, K, _ptr(ids), T, top_k, _ptr(x_packed), x_rows,
+          x_tok_rows, x_slot_rows, _ptr(Y), _stream(stream))
+
+
+def bqm_route(score, logits, l_stride: int, bias, T: int, E: int, n_group: int, topk_group: int,
+              group_top: int, top_k: int, renorm: bool, scale: float, ids, weights, stream=None):
+    """score: "softmax" or "sigmoid"; logits of fp32, fp16 or bf16, rows l_stride elements apart; bias: fp32 or None."""
+    _call("bqm_route", SCORE.get(score, -1), _type(logits), _ptr(logits), l_stride, _ptr(bias), T, E, n_group,
+          topk_group, group_top, top_k, int(renorm), scale, _ptr(ids), _ptr(weights), _stream(stream))
 
 
 class Gemv(ctypes.Structure):

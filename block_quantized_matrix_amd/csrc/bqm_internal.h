@@ -40,6 +40,28 @@ inline bool layout_of(int fmt, int64_t rows, int64_t K, Layout* L) {
   return true;
 }
 
+// Packed layout of a rows x K MXFP4 matrix (mxfp4.h describes it): rt tiles of 16 rows, ks steps
+// of 128 k, kg groups of four steps; 1024 code bytes per tile and step, then 256 scale bytes per
+// tile and group of steps.
+struct MxLayout {
+  int64_t rt, ks, kg;
+  int64_t scales_off;
+  int64_t total;
+};
+
+inline MxLayout mx_layout(int64_t rows, int64_t K) {
+  MxLayout L;
+  L.rt = (rows + 15) / 16;
+  L.ks = (K + 127) / 128;
+  L.kg = (K + 511) / 512;
+  L.scales_off = L.rt * L.ks * 1024;
+  L.total = L.scales_off + L.rt * L.kg * 256;
+  return L;
+}
+
+// Workgroups of a launch: HIP counts a launch's threads in 32 bits (at most 1024 a workgroup here).
+constexpr int64_t kMaxGrid = ((int64_t)1 << 22) - 1;
+
 inline int interchange_block_bytes(int fmt) { return fmt == BQM_Q4_0 ? 18 : 34; }
 
 inline int launch_status() {
@@ -71,6 +93,20 @@ int launch_qmm_q4_0(const void* w, const int8_t* Xq, const float* dx, float* Y, 
 int launch_qmm_id(int fmt, const void* w, int E, int64_t N, int64_t K, const int32_t* ids, int T,
                   int top_k, const int8_t* Xq, const float* dx, int64_t x_tok_rows,
                   int64_t x_slot_rows, float* Y, hipStream_t s);
+int launch_repack_mxfp4(const void* src, void* dst, int64_t rows, int64_t K, hipStream_t s);
+int launch_unpack_mxfp4(const void* src, void* dst, int64_t rows, int64_t K, hipStream_t s);
+int launch_quantize_mxfp4(int type, const void* X, int64_t stride, void* packed, int64_t rows, int64_t K,
+                          hipStream_t s);
+int launch_dequantize_mxfp4(const void* packed, int type, void* Y, int64_t stride, int64_t rows, int64_t K,
+                            hipStream_t s);
+int launch_qmv_mxfp4(const void* w, const float* X, float* Y, int M, int64_t N, int64_t K, hipStream_t s);
+int launch_qmm_mxfp4(const void* w, const void* x, float* Y, int64_t M, int64_t N, int64_t K, hipStream_t s);
+int launch_qmm_id_mxfp4(const void* w, int E, int64_t N, int64_t K, const int32_t* ids, int T, int top_k,
+                        const void* x, int64_t x_rows, int64_t x_tok_rows, int64_t x_slot_rows, float* Y,
+                        hipStream_t s);
+int launch_route(int score, int type, const void* logits, int64_t stride, const float* bias, int64_t T, int E,
+                 int n_group, int topk_group, int group_top, int top_k, int renorm, float scale, int32_t* ids,
+                 float* weights, hipStream_t s);
 int launch_fill(float* y, int64_t n, float v, hipStream_t s);
 int cu_count();
 int launch_id_mma(int fmt, const void* w, const void* w_up, int E, int64_t N, int64_t K,

@@ -98,3 +98,6 @@ int launch_unpack(int fmt, const void* src, void* dst, int64_t rows, int64_t K, 
 }
 
 }  // namespace bqm
+
+#include "mxfp4_pack.h"
+#include "route.h"

@@ -8,6 +8,8 @@
  *     y = dequant(W) . x
  * with W stored in 32-weight blocks that each carry one binary16 scale d:
  *     Q4_0 weight = (nibble - 8) * d        Q8_0 weight = int8 * d.
+ * A third format, MXFP4, carries a power of two per block and has its own products; and
+ * bqm_route makes the expert ids and weights that the indexed products take.
  *
  * Interchange block layout (host or device bytes, what bqm_repack reads):
  *     Q4_0: 18 bytes per block = binary16 d (little endian), then 16 bytes; byte j
@@ -64,7 +66,13 @@ typedef enum {
   BQM_E_LAUNCH = 5       /* the HIP runtime refused a launch                    */
 } bqm_status;
 
-typedef enum { BQM_Q4_0 = 2, BQM_Q8_0 = 8 } bqm_fmt;
+/* Block formats.  BQM_MXFP4 is taken by bqm_packed_bytes, bqm_repack and bqm_unpack, and has
+ * products of its own (the *_mxfp4 calls); the calls with a fmt argument other than those three
+ * refuse it with BQM_E_UNSUPPORTED. */
+typedef enum { BQM_Q4_0 = 2, BQM_Q8_0 = 8, BQM_MXFP4 = 39 } bqm_fmt;
+
+/* Element types of float rows (router logits, the rows of the MXFP4 quantizer). */
+typedef enum { BQM_F32 = 0, BQM_F16 = 1, BQM_BF16 = 30 } bqm_type;
 
 /* Largest M accepted by qmv_q4_0 / qmv_q8_0, the small-batch decode width. */
 #define BQM_QMV_MAX_M 8
@@ -270,6 +278,82 @@ int qmm_q4_0(const void* w_packed, const int8_t* Xq, const float* dx, float* Y, 
 int qmm_id(int fmt, const void* w_packed, int E, int64_t N, int64_t K, const int32_t* ids, int T,
            int top_k, const int8_t* Xq, const float* dx, int64_t x_tok_rows, int64_t x_slot_rows,
            float* Y, hipStream_t stream);
+
+/* ---- MXFP4 ----------------------------------------------------------------------------
+ * The OCP microscaling format with 4-bit elements, the one block format that the matrix cores
+ * of gfx950 multiply as it is stored: 32 e2m1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 for the low
+ * three bits, negative with the fourth) under one e8m0 scale byte e that stands for 2^(e - 127),
+ * e = 255 for NaN.  Interchange block: 17 bytes, e first, then 16 bytes of which byte j holds code
+ * j in its low nibble and code j + 16 in its high one (any alignment).  Packed: as for the other
+ * formats, written by bqm_repack and also by bqm_quantize_mxfp4; one layout serves weights and
+ * activations.  4.25 bits per weight, rows padded to 16 and K to 128 (codes) and 512 (scales). */
+
+/* Rows of floats -> packed MXFP4.  Per row and block of 32, in the values of x_type: m = max |x|;
+ * the scale is 2^s with s = floor(log2 m) - 2, at least -127 (m = 0: -127); each code is the e2m1
+ * value nearest to x / 2^s, ties to the even code, values beyond 6 to 6, signs kept.  A block with
+ * an infinity or a NaN gets the scale byte 255 and codes 0.  Bit exact.
+ * X: [rows][K] of x_type (bqm_type) with x_stride elements from row to row; X 16-byte aligned,
+ * rows 16-byte aligned or not.  packed: bqm_packed_bytes(BQM_MXFP4, rows, K) bytes, all written.
+ * x_stride < K: BQM_E_SHAPE; an unknown type: BQM_E_UNSUPPORTED. */
+int bqm_quantize_mxfp4(int x_type, const void* X, int64_t x_stride, void* packed, int64_t rows, int64_t K,
+                       hipStream_t stream);
+
+/* Packed MXFP4 -> rows of floats, each value rounded once to y_type (exact in fp32 and bf16 but for
+ * scales above 2^125 whose values pass the type's range and become infinities; the values of a
+ * block with scale byte 255 are NaN).  Y: [rows][K] with y_stride elements from row to row, the
+ * elements between rows are left as they are. */
+int bqm_dequantize_mxfp4(const void* packed, int y_type, void* Y, int64_t y_stride, int64_t rows, int64_t K,
+                         hipStream_t stream);
+
+/* Decode GEMV and small-batch GEMV with MXFP4 weights, qmv_q4_0's counterpart:
+ *     Y[m][n] = sum_k dequant(W)[n][k] * X[m][k],   0 <= m < M <= 8, 0 <= n < N,   X and Y fp32.
+ * Same tolerance and status codes. */
+int qmv_mxfp4(const void* w_packed, const float* X, float* Y, int M, int64_t N, int64_t K, hipStream_t stream);
+
+/* Prefill product of two packed MXFP4 matrices, qmm_q4_0's counterpart:
+ *     Y[m][n] = sum_k dequant(W)[n][k] * dequant(X)[m][k]                 fp32
+ * w_packed: packed N x K.  x_packed: packed M x K, from bqm_quantize_mxfp4.  Products of codes are
+ * exact and block scales are powers of two; the sums are fp32.  Any M from one token on.  A block
+ * of either operand with scale byte 255 makes the outputs of its row NaN. */
+int qmm_mxfp4(const void* w_packed, const void* x_packed, float* Y, int64_t M, int64_t N, int64_t K, hipStream_t stream);
+
+/* Expert-indexed qmm_mxfp4, qmm_id's counterpart:
+ *     e = ids[t][s],  r = t * x_tok_rows + s * x_slot_rows,
+ *     Y[t][s][n] = sum_k dequant(W)[e][n][k] * dequant(X)[r][k]
+ * w_packed: expert tensor packed as ONE matrix of E*N rows.  x_packed: packed x_rows x K; every
+ * row that the slots address lies below x_rows (else BQM_E_SHAPE).  Padding slots (negative id) give
+ * zero rows, ids >= E NaN rows.  Limits: T <= BQM_QMM_ID_MAX_T, top_k <= 32, E <= 4096. */
+int qmm_id_mxfp4(const void* w_packed, int E, int64_t N, int64_t K, const int32_t* ids, int T, int top_k,
+                 const void* x_packed, int64_t x_rows, int64_t x_tok_rows, int64_t x_slot_rows, float* Y,
+                 hipStream_t stream);
+
+/* ---- routing to experts ----------------------------------------------------------------
+ * The ids and weights that qmv_id, qmv_id_gate_up, qmv_id_sum, qmm_id and qmm_id_mxfp4 take, from
+ * a router's logits (the top-k routed experts of the page "ik_llama.cpp 老工作站多 GPU 部署
+ * Qwen3-235B-A22B 实战指南" (nxmr.cn), background section).  Per token:
+ *     score[e] = softmax over the E logits, or 1 / (1 + exp(-logit[e]))
+ *     value[e] = logit[e] without a bias, score[e] + bias[e] with one
+ * n_group > 1: the experts form n_group runs of E / n_group; a group's value is the sum of its
+ * group_top (1 or 2) largest value[e] (of score[e] where group_top is 2 and there is no bias), and
+ * only the experts of the topk_group groups with the largest take part.  The top_k experts with the
+ * largest value are chosen, in descending order, ties (of groups too) to the lower index:
+ *     ids[t][s] = e,   weights[t][s] = scale * score[e]  (/ the sum of the chosen scores with renorm)
+ * Values are compared in 64 bits, so that neighbours come out in the order of the real numbers.
+ * An expert whose logit (or bias) is -infinity is never chosen; slots that no expert is left
+ * for get id -1 (a padding slot of the products) and weight 0.  Chosen scores that sum to 0 give
+ * weights 0.  A NaN logit or bias, or with softmax a logit of +infinity, gives that token the ids
+ * 0, 1, ... and NaN weights.
+ * logits: [T][E] of l_type (bqm_type) with l_stride >= E elements from row to row.  bias: fp32 [E] or
+ * NULL.  ids: int32 [T][top_k], weights: fp32 [T][top_k].  All pointers aligned to 16 bytes but
+ * bias (4).  Limits: E <= 4096, top_k <= 32, n_group <= BQM_ROUTE_MAX_GROUPS dividing E,
+ * 1 <= topk_group <= n_group, group_top 1 or 2 and at most E / n_group where n_group > 1,
+ * T <= BQM_ROUTE_MAX_T.  E = 0: every id -1.  Unknown score or type: BQM_E_UNSUPPORTED. */
+typedef enum { BQM_SOFTMAX = 0, BQM_SIGMOID = 1 } bqm_score;
+#define BQM_ROUTE_MAX_GROUPS 64
+#define BQM_ROUTE_MAX_T (1 << 22)
+int bqm_route(int score, int l_type, const void* logits, int64_t l_stride, const float* bias, int T, int E,
+              int n_group, int topk_group, int group_top, int top_k, int renorm, float scale, int32_t* ids,
+              float* weights, hipStream_t stream);
 
 /* Static English text for a status code. */
 const char* bqm_strerror(int status);
