@@ -7,11 +7,13 @@
 // lane l: row l % 16, block l / 16 of the four that the instruction covers) and its scale in a
 // byte of a register.  The packed layout is made of that instruction's operands:
 //
-//   codes   [row tile of 16][step of 128 k][row][64 bytes]: an operand is 1024 contiguous
-//           bytes; a row's share of it, four blocks of 16 bytes, is contiguous too
-//   scales  [row tile of 16][four steps][row][block in step][step]: one 4-byte word per lane
+//   codes   [row tile of 16][step of 128 k][block in step][row][16 bytes]: an operand is 1024
+//           contiguous bytes in lane order, one load of 16 bytes per lane
+//   scales  [row tile of 16][four steps][block in step][row][step]: one 4-byte word per lane
 //           holds the scales of four steps, which the instruction picks its byte from
 //
+// (With a row's four blocks next to each other, 64 bytes, the lanes of a load are 64 bytes apart
+// and a wave's 1024 bytes take the address unit four times as long.)
 // The order of the codes inside a block is the interchange one (byte j: code j low, code
 // j + 16 high); a dot product of two such blocks does not depend on it.  Rows are padded to 16,
 // K to 128 in the codes and to 512 in the scales, with codes 0 and scales 1.
@@ -36,10 +38,10 @@ constexpr uint8_t kOne = 127;       // the scale 1
 constexpr uint8_t kNanScale = 255;
 
 __host__ __device__ __forceinline__ int64_t code_at(int64_t row, int64_t b, int64_t ks) {
-  return ((row >> 4) * ks + (b >> 2)) * kOperand + (row & 15) * 64 + (b & 3) * 16;
+  return ((row >> 4) * ks + (b >> 2)) * kOperand + (b & 3) * 256 + (row & 15) * 16;
 }
 __host__ __device__ __forceinline__ int64_t scale_at(int64_t row, int64_t b, int64_t kg) {
-  return ((row >> 4) * kg + (b >> 4)) * kScaleTile + (row & 15) * 16 + (b & 3) * 4 + ((b >> 2) & 3);
+  return ((row >> 4) * kg + (b >> 4)) * kScaleTile + (b & 3) * 64 + (row & 15) * 4 + ((b >> 2) & 3);
 }
 
 // 2^(byte - 127) as a float (byte 0 is subnormal), NaN for 255

@@ -314,7 +314,9 @@ int qmv_mxfp4(const void* w_packed, const float* X, float* Y, int M, int64_t N, 
  *     Y[m][n] = sum_k dequant(W)[n][k] * dequant(X)[m][k]                 fp32
  * w_packed: packed N x K.  x_packed: packed M x K, from bqm_quantize_mxfp4.  Products of codes are
  * exact and block scales are powers of two; the sums are fp32.  Any M from one token on.  A block
- * of either operand with scale byte 255 makes the outputs of its row NaN. */
+ * of either operand with scale byte 255 makes the outputs of its row NaN.  K above
+ * BQM_MXFP4_MAX_K: BQM_E_SHAPE (qmm_id_mxfp4 too, and where the activations' codes reach 2 GiB). */
+#define BQM_MXFP4_MAX_K (1 << 23)
 int qmm_mxfp4(const void* w_packed, const void* x_packed, float* Y, int64_t M, int64_t N, int64_t K, hipStream_t stream);
 
 /* Expert-indexed qmm_mxfp4, qmm_id's counterpart:
