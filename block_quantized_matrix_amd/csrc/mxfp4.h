@@ -55,6 +55,15 @@ __device__ __forceinline__ f32x2 pair_of(uint32_t word, float scale) {
   return __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(word, scale, B);
 }
 
+// Between what a wave writes to LDS and other lanes of it read there, and before the place is
+// written again.  (A wave's LDS operations keep their order; this keeps the compiler, which sees one
+// lane's addresses, from changing it.)
+__device__ __forceinline__ void wave_turn() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // Element types of float rows (the codes of bqm_type).
 template <int TYPE>
 struct Elem;

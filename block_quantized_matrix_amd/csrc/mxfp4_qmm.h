@@ -219,7 +219,7 @@ __device__ __forceinline__ void mx_core(const MxOperand& W, const MxOperand& X, 
   for (int t = 0; t < TM; t++) {
 #pragma unroll
     for (int u = 0; u < TN; u++) *reinterpret_cast<MxAcc*>(own + i * kRow + u * 16 + 4 * q) = acc[u][t];
-    if (KS > 1) __syncthreads();
+    KS > 1 ? __syncthreads() : mx::wave_turn();
     if ((N & 3) == 0) {
 #pragma unroll
       for (int r = 0; r < TN; r++) {
@@ -244,7 +244,7 @@ __device__ __forceinline__ void mx_core(const MxOperand& W, const MxOperand& X, 
         if (y && nw + n < N) y[nw + n] = d;
       }
     }
-    if (KS > 1) __syncthreads();
+    KS > 1 ? __syncthreads() : mx::wave_turn();
   }
 }
 

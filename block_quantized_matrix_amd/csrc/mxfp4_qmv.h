@@ -1,54 +1,225 @@
 // Decode product with MXFP4 weights (kernel and launcher; included by qmv_mma.hip):
 //   Y[m][n] = sum_b 2^(e[n][b] - 127) sum_{j<32} c[n][32b+j] X[m][32b+j],   M <= 8, fp32 X and Y.
+//
+// HBM binds it (4.25 bits a weight), so the vector work per weight has to stay small.  Codes are
+// converted two at a time to bf16 with their block's scale in place, exact, and go to
+// v_mfma_f32_16x16x32_bf16 as its rows.  (The fp4 x fp8 instruction would take them as they are, but
+// it drops products below 2^-13 of the largest beside them: inputs in fp8 parts lose too much.)  Each
+// input is split into three bf16 parts, together exactly x; the parts of up to five inputs are 15 of
+// the 16 columns of one instruction, those of six to eight take two.  Products of bf16 are exact in
+// fp32, so what is left is the rounding of fp32 sums.
 #pragma once
 
+#include "mma_ops.h"
 #include "mxfp4.h"
 
 namespace bqm {
 namespace {
 
-// One wave per row: lane b takes the blocks b, b + 64, ..., the lanes' sums are added at the end.
-__global__ __launch_bounds__(256) void k_qmv_mxfp4(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
-                                                   const float* __restrict__ X, float* __restrict__ Y, int M, int64_t N,
-                                                   int64_t K, int64_t ks, int64_t kg) {
-  const int lane = threadIdx.x & 63;
-  const int64_t row = blockIdx.x * (int64_t)4 + (threadIdx.x >> 6);
-  if (row >= N) return;
-  float acc[BQM_QMV_MAX_M] = {};
-  for (int64_t b = lane; b < K / kQK; b += 64) {
-    const mx::u32x4 v = *reinterpret_cast<const mx::u32x4*>(codes + mx::code_at(row, b, ks));
-    const float s = mx::scale_of(scales[mx::scale_at(row, b, kg)]);
-    for (int m = 0; m < BQM_QMV_MAX_M; m++) {
-      if (m >= M) break;
-      const float* x = X + m * K + b * 32;
-      float c = 0;
+constexpr uint32_t kMxOob = 0x80000000u;  // an offset past every descriptor: reads 0
+
+struct MxvArgs {
+  const uint8_t* w;
+  const float* x;
+  float* y;
+  int64_t scales_off, N, K, tiles;
+  int M, ks, kg, halves;
+};
+
+// The three bf16 parts of eight inputs, a[j] and b[j] the pair of word j: each part the upper half of
+// what the parts before it leave.
+template <bool ODD>
+__device__ __forceinline__ void mxv_parts(const float (&a)[4], const float (&b)[4], mx::u32x4 (&part)[3]) {
 #pragma unroll
-      for (int j = 0; j < 4; j++) {
-        const mx::f32x2 p[4] = {mx::pair_of<0>(v[j], 1.0f), mx::pair_of<1>(v[j], 1.0f), mx::pair_of<2>(v[j], 1.0f),
-                                mx::pair_of<3>(v[j], 1.0f)};
+  for (int j = 0; j < 4; j++) {
+    float f[2] = {a[j], b[j]};
 #pragma unroll
-        for (int k = 0; k < 4; k++) c = fmaf(p[k].y, x[4 * j + k + 16], fmaf(p[k].x, x[4 * j + k], c));
+    for (int p = 0; p < 3; p++) {
+      uint32_t u[2];
+#pragma unroll
+      for (int k = 0; k < 2; k++) {
+        u[k] = __float_as_uint(f[k]);
+        if (ODD && f[k] != f[k]) u[k] |= 0x00400000u;  // a payload in the low half must not leave an infinity
+        if (p < 2) f[k] -= __uint_as_float(u[k] & 0xFFFF0000u);
+        if (ODD && !__builtin_isfinite(f[k])) f[k] = 0;  // nothing is left of an infinity or a NaN
       }
-      acc[m] = fmaf(s, c, acc[m]);
+      part[p][j] = __builtin_amdgcn_perm(u[1], u[0], 0x07060302u);
     }
   }
-  for (int m = 0; m < BQM_QMV_MAX_M; m++) {
-    if (m >= M) break;
-    float a = acc[m];
-    for (int o = 32; o > 0; o >>= 1) a += __shfl_xor(a, o, 64);
-    if (lane == 0) Y[m * N + row] = a;
+}
+__device__ __forceinline__ void mxv_split(const float (&a)[4], const float (&b)[4], mx::u32x4 (&part)[3]) {
+  float probe = 0;
+#pragma unroll
+  for (int j = 0; j < 4; j++) probe = fmaf(a[j], 0.0f, fmaf(b[j], 0.0f, probe));  // NaN if any is not finite
+  if (__any(probe != probe))
+    mxv_parts<true>(a, b, part);
+  else
+    mxv_parts<false>(a, b, part);
+}
+
+// A workgroup takes `halves` runs of eight rows (a run is a whole 128-byte line of a step's codes),
+// at most T tiles of 16, its W waves the steps of 128 k in turn: wave w the steps w, w + W, ...  A
+// wave splits the inputs of its step once (R items of eight a lane), turns them to the
+// instruction's columns (CT of 16) through LDS of its own, and multiplies all the workgroup's
+// tiles by them; loads run D steps ahead.  No wave waits for another until the end, when the
+// waves' sums are added in order.
+template <int R, int CT, int T, int D, int W, int OCC>
+__global__ __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(OCC, OCC))) void k_qmv_mxfp4(MxvArgs a) {
+  constexpr int kCols = CT * 16;
+  constexpr int kTurn = 16 * (CT == 1 ? 15 : 25) * 16;  // bytes: 16 lots of eight inputs, the columns in use
+  constexpr int kSums = T * kCols * 16 * 4;              // bytes of a wave's sums: [tile][column][row]
+  constexpr int kWave = kTurn > kSums ? kTurn : kSums;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[W * kWave];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int i = lane & 15, q = lane >> 4;
+  const int cols = 3 * a.M, lot = (cols | 1) * 16;  // bytes of a lot; an odd count of 16: no bank conflicts
+  const int64_t r0 = (int64_t)blockIdx.x * a.halves * 8, t0 = r0 >> 4;
+  const int64_t r1 = r0 + a.halves * 8 < a.N ? r0 + a.halves * 8 : a.N;
+  const int64_t cb = (a.tiles - t0) * a.ks * mx::kOperand, sb = (a.tiles - t0) * a.kg * mx::kScaleTile, most = 0x7FFFFFFF;
+  const __amdgpu_buffer_rsrc_t rc =
+      __builtin_amdgcn_make_buffer_rsrc((void*)(a.w + t0 * a.ks * mx::kOperand), 0, (int)(cb < most ? cb : most), 0x00020000);
+  const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc((void*)(a.w + a.scales_off + t0 * a.kg * mx::kScaleTile), 0,
+                                                                      (int)(sb < most ? sb : most), 0x00020000);
+  const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc((void*)a.x, 0, (int)(a.M * a.K * 4), 0x00020000);
+  uint32_t oc[T], os[T];
+#pragma unroll
+  for (int t = 0; t < T; t++) {
+    const int64_t row = (t0 + t) * 16 + i;
+    const bool in = row >= r0 && row < r1;
+    oc[t] = in ? (uint32_t)(t * a.ks * mx::kOperand + lane * 16) : kMxOob;
+    os[t] = in ? (uint32_t)(t * a.kg * mx::kScaleTile + lane * 4) : kMxOob;
   }
+  const int nb = (int)(a.K / kQK);
+  mx::u32x4 code[D][T], xa[D][R], xb[D][R];
+  uint32_t scale[D][T];
+  uint32_t ox[R];
+#pragma unroll
+  for (int r = 0; r < R; r++) {
+    const int item = r * 64 + lane, m = item >> 4;
+    ox[r] = m < a.M ? (uint32_t)(m * (int)a.K + (item >> 2 & 3) * 32 + (item & 3) * 4) * 4 : kMxOob;
+  }
+  // a step past the last reads zeros
+  auto load_x = [&](int d, int s) {
+    const bool any = s < a.ks;
+#pragma unroll
+    for (int r = 0; r < R; r++) {
+      const uint32_t at = 4 * s + (lane >> 2 & 3) < nb ? ox[r] : kMxOob;  // and so does a block past the row's end
+      xa[d][r] = __builtin_amdgcn_raw_buffer_load_b128(rx, at, any ? s * 512 : 0, 0);
+      xb[d][r] = __builtin_amdgcn_raw_buffer_load_b128(rx, at + 64, any ? s * 512 : 0, 0);
+    }
+  };
+  auto load_w = [&](int d, int t, int s) {
+    const bool any = s < a.ks;
+    code[d][t] = __builtin_amdgcn_raw_buffer_load_b128(rc, any ? oc[t] : kMxOob, any ? s * mx::kOperand : 0, 0);
+    scale[d][t] = __builtin_amdgcn_raw_buffer_load_b8(rs, any ? os[t] : kMxOob, any ? (s >> 2) * mx::kScaleTile + (s & 3) : 0, 0);
+  };
+  uint8_t* mine = lds + wave * kWave;
+  mx::f32x4 acc[T][CT] = {};
+#pragma unroll
+  for (int d = 0; d < D; d++) {
+    load_x(d, wave + d * W);
+#pragma unroll
+    for (int t = 0; t < T; t++) load_w(d, t, wave + d * W);
+  }
+  for (int s0 = wave; s0 < a.ks; s0 += D * W) {
+#pragma unroll
+    for (int d = 0; d < D; d++) {
+      const int s = s0 + d * W;
+#pragma unroll
+      for (int r = 0; r < R; r++) {
+        const int item = r * 64 + lane, m = item >> 4, at = (item & 3) * 4 + (item >> 2 & 3);
+        float fa[4], fb[4];
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+          fa[j] = __uint_as_float(xa[d][r][j]);
+          fb[j] = __uint_as_float(xb[d][r][j]);
+        }
+        mx::u32x4 part[3];
+        mxv_split(fa, fb, part);
+        if (m < a.M)
+#pragma unroll
+          for (int p = 0; p < 3; p++) *reinterpret_cast<mx::u32x4*>(mine + at * lot + (3 * m + p) * 16) = part[p];
+      }
+      load_x(d, s + D * W);  // loads are issued in the order of their use, each as soon as its registers are free
+      mx::wave_turn();
+      mma::bf16x8 b[4][CT];
+#pragma unroll
+      for (int t = 0; t < 4; t++)
+#pragma unroll
+        for (int c = 0; c < CT; c++) {
+          const int col = c * 16 + i < cols ? c * 16 + i : cols - 1;  // columns not in use repeat one that is
+          b[t][c] = *reinterpret_cast<const mma::bf16x8*>(mine + (t * 4 + q) * lot + col * 16);
+        }
+#pragma unroll
+      for (int t = 0; t < T; t++) {
+        const float f = __uint_as_float(scale[d][t] << 23);  // the conversion goes by the exponent field alone
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+          typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+          const uint32_t word = code[d][t][k];
+          const bf16x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(word, f, 0), p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(word, f, 1),
+                       p2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(word, f, 2), p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(word, f, 3);
+          const mma::bf16x8 w{p0.x, p0.y, p1.x, p1.y, p2.x, p2.y, p3.x, p3.y};
+#pragma unroll
+          for (int c = 0; c < CT; c++) acc[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, b[k][c], acc[t][c], 0, 0, 0);
+        }
+        load_w(d, t, s + D * W);
+      }
+      mx::wave_turn();  // the next step's inputs go where these were read
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < T; t++)
+#pragma unroll
+    for (int c = 0; c < CT; c++)
+      *reinterpret_cast<mx::f32x4*>(mine + ((t * kCols + c * 16 + i) * 16 + 4 * q) * 4) = acc[t][c];
+  __syncthreads();
+  for (int o = threadIdx.x; o < T * 16 * a.M; o += W * 64) {
+    const int row = o % (T * 16), m = o / (T * 16);
+    const int64_t n = t0 * 16 + row;
+    if (n < r0 || n >= r1) continue;
+    float part[3] = {};
+#pragma unroll
+    for (int w = 0; w < W; w++)
+#pragma unroll
+      for (int p = 0; p < 3; p++)
+        part[p] += *reinterpret_cast<const float*>(lds + w * kWave + (((row >> 4) * kCols + 3 * m + p) * 16 + (row & 15)) * 4);
+    a.y[m * a.N + n] = part[0] + (part[1] + part[2]);
+  }
+}
+
+template <int R, int CT, int T, int D, int W, int OCC>
+int launch_mxv_as(const MxvArgs& a, int64_t grid, hipStream_t s) {
+  hipLaunchKernelGGL((k_qmv_mxfp4<R, CT, T, D, W, OCC>), dim3((unsigned)grid), dim3(W * 64), 0, s, a);
+  return launch_status();
+}
+template <int R, int CT>
+int launch_mxv(const MxvArgs& a, int64_t grid, hipStream_t s) {
+  const int T = (a.halves + 1) / 2;
+  return T <= 1   ? launch_mxv_as<R, CT, 1, 2, 16, 4>(a, grid, s)
+         : T <= 2 ? launch_mxv_as<R, CT, 2, 1, 16, 4>(a, grid, s)
+         : T <= 3 ? launch_mxv_as<R, CT, 3, 1, 8, 2>(a, grid, s)
+         : T <= 5 ? launch_mxv_as<R, CT, 5, 1, 8, 2>(a, grid, s)
+         : T <= 7 ? launch_mxv_as<R, CT, 7, 1, 8, 2>(a, grid, s)
+                  : launch_mxv_as<R, CT, 9, 1, 8, 2>(a, grid, s);
 }
 
 }  // namespace
 
+// One workgroup per compute unit, or as many rounds of them as nine tiles each make, so that all end
+// together: sixteen waves where a unit has up to two tiles of rows, eight with registers for more
+// tiles above.  Measured (us): 4096 x 4096, one input, 4.8 (eight waves 5.7; two workgroups a
+// unit 7.5); 5120 x 17408 at batch 8 20.2 (eight waves 22.0, two a unit 31.9); 34816 x 5120
+// with eight waves 20.1, 4.7 TB/s (sixteen and two rounds 27.1), at batch 8 24.3 (38.8).  Loads
+// two steps ahead instead of one gained nothing from three tiles on (34816 x 5120: 22.8).
 int launch_qmv_mxfp4(const void* w, const float* X, float* Y, int M, int64_t N, int64_t K, hipStream_t s) {
   const MxLayout L = mx_layout(N, K);
-  const uint8_t* codes = static_cast<const uint8_t*>(w);
-  const int64_t grid = (N + 3) / 4;
+  if (K > BQM_MXFP4_MAX_K) return BQM_E_SHAPE;
+  const int64_t runs = (N + 7) / 8, rounds = (runs + 256 * 17 - 1) / (256 * 17);
+  const int64_t halves = (runs + 256 * rounds - 1) / (256 * rounds), grid = (runs + halves - 1) / halves;
   if (grid > kMaxGrid) return BQM_E_SHAPE;
-  hipLaunchKernelGGL(k_qmv_mxfp4, dim3((unsigned)grid), dim3(256), 0, s, codes, codes + L.scales_off, X, Y, M, N, K, L.ks, L.kg);
-  return launch_status();
+  const MxvArgs a{static_cast<const uint8_t*>(w), X, Y, L.scales_off, N, K, L.rt, M, (int)L.ks, (int)L.kg, (int)halves};
+  return M <= 4 ? launch_mxv<1, 1>(a, grid, s) : M == 5 ? launch_mxv<2, 1>(a, grid, s) : launch_mxv<2, 2>(a, grid, s);
 }
 
 }  // namespace bqm
