@@ -92,21 +92,23 @@ def strerror(status: int) -> str:
 
 
 def _ptr(t):
-    if t is None:
-        return None
-    if isinstance(t, int):
-        return ctypes.c_void_p(t)
-    return ctypes.c_void_p(t.data_ptr()) if t.numel() > 0 else ctypes.c_void_p(t.data_ptr() or None)
+    return t if t is None or isinstance(t, int) else t.data_ptr()
 
 
 def _stream(stream):
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())  # current_stream() without its object
+    return stream.cuda_stream
+
+
+_fns = {}
 
 
 def _call(name, *args):
-    st = getattr(lib(), name)(*args)
+    fn = _fns.get(name)
+    if fn is None:
+        fn = _fns[name] = getattr(lib(), name)
+    st = fn(*args)
     if st != 0:
         raise BqmError(name, st)
 
@@ -181,35 +183,45 @@ def _type(t):
     return TYPE.get(t.dtype, -1)  # the library refuses an unknown type
 
 
+def _call_on(t, stream, name, *args):
+    """The call on t's device, where that is another than the current one too."""
+    d = t.device.index if isinstance(t, torch.Tensor) else None
+    if d is None or d == torch.cuda.current_device():
+        _call(name, *args, _stream(stream))
+    else:
+        with torch.cuda.device(d):
+            _call(name, *args, _stream(stream))
+
+
 def bqm_quantize_mxfp4(X, x_stride: int, packed, rows: int, K: int, stream=None):
     """Rows of fp32, fp16 or bf16 (by X's dtype), x_stride elements apart -> packed MXFP4."""
-    _call("bqm_quantize_mxfp4", _type(X), _ptr(X), x_stride, _ptr(packed), rows, K, _stream(stream))
+    _call_on(packed, stream, "bqm_quantize_mxfp4", _type(X), _ptr(X), x_stride, _ptr(packed), rows, K)
 
 
 def bqm_dequantize_mxfp4(packed, Y, y_stride: int, rows: int, K: int, stream=None):
     """Packed MXFP4 -> rows of Y's dtype, y_stride elements apart."""
-    _call("bqm_dequantize_mxfp4", _ptr(packed), _type(Y), _ptr(Y), y_stride, rows, K, _stream(stream))
+    _call_on(Y, stream, "bqm_dequantize_mxfp4", _ptr(packed), _type(Y), _ptr(Y), y_stride, rows, K)
 
 
 def qmv_mxfp4(w_packed, X, Y, M: int, N: int, K: int, stream=None):
-    _call("qmv_mxfp4", _ptr(w_packed), _ptr(X), _ptr(Y), M, N, K, _stream(stream))
+    _call_on(Y, stream, "qmv_mxfp4", _ptr(w_packed), _ptr(X), _ptr(Y), M, N, K)
 
 
 def qmm_mxfp4(w_packed, x_packed, Y, M: int, N: int, K: int, stream=None):
-    _call("qmm_mxfp4", _ptr(w_packed), _ptr(x_packed), _ptr(Y), M, N, K, _stream(stream))
+    _call_on(Y, stream, "qmm_mxfp4", _ptr(w_packed), _ptr(x_packed), _ptr(Y), M, N, K)
 
 
 def qmm_id_mxfp4(w_packed, E: int, N: int, K: int, ids, T: int, top_k: int, x_packed, x_rows: int,
                  x_tok_rows: int, x_slot_rows: int, Y, stream=None):
-    _call("qmm_id_mxfp4", _ptr(w_packed), E, N, K, _ptr(ids), T, top_k, _ptr(x_packed), x_rows,
-          x_tok_rows, x_slot_rows, _ptr(Y), _stream(stream))
+    _call_on(Y, stream, "qmm_id_mxfp4", _ptr(w_packed), E, N, K, _ptr(ids), T, top_k, _ptr(x_packed), x_rows,
+          x_tok_rows, x_slot_rows, _ptr(Y))
 
 
 def bqm_route(score, logits, l_stride: int, bias, T: int, E: int, n_group: int, topk_group: int,
               group_top: int, top_k: int, renorm: bool, scale: float, ids, weights, stream=None):
     """score: "softmax" or "sigmoid"; logits of fp32, fp16 or bf16, rows l_stride elements apart; bias: fp32 or None."""
-    _call("bqm_route", SCORE.get(score, -1), _type(logits), _ptr(logits), l_stride, _ptr(bias), T, E, n_group,
-          topk_group, group_top, top_k, int(renorm), scale, _ptr(ids), _ptr(weights), _stream(stream))
+    _call_on(ids, stream, "bqm_route", SCORE.get(score, -1), _type(logits), _ptr(logits), l_stride, _ptr(bias), T, E, n_group,
+          topk_group, group_top, top_k, int(renorm), scale, _ptr(ids), _ptr(weights))
 
 
 class Gemv(ctypes.Structure):

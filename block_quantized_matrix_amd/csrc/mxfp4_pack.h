@@ -9,9 +9,10 @@ namespace {
 
 using namespace mx;
 
-constexpr int kPackThreads = 256;
+constexpr int kPackThreads = 256, kPackWaves = kPackThreads / 64;
 constexpr int kPackGrid = 1 << 16;  // workgroups of a launch at most; each takes every kPackGrid-th
 
+// One lane per block and padding block.  The 17-byte blocks are read as unaligned words.
 __global__ __launch_bounds__(kPackThreads) void k_repack_mxfp4(const uint8_t* __restrict__ src, uint8_t* __restrict__ codes,
                                                                uint8_t* __restrict__ scales, int64_t rows, int64_t nb,
                                                                int64_t ks, int64_t kg, int64_t total) {
@@ -22,10 +23,7 @@ __global__ __launch_bounds__(kPackThreads) void k_repack_mxfp4(const uint8_t* __
     scales[scale_at(row, b, kg)] = real ? s[0] : kOne;
     if (b >= ks * 4) continue;
     u32x4 v{0, 0, 0, 0};
-    if (real)
-#pragma unroll
-      for (int k = 0; k < 4; k++)
-        v[k] = (uint32_t)s[1 + 4 * k] | (uint32_t)s[2 + 4 * k] << 8 | (uint32_t)s[3 + 4 * k] << 16 | (uint32_t)s[4 + 4 * k] << 24;
+    if (real) __builtin_memcpy(&v, s + 1, 16);
     *reinterpret_cast<u32x4*>(codes + code_at(row, b, ks)) = v;
   }
 }
@@ -37,66 +35,130 @@ __global__ __launch_bounds__(kPackThreads) void k_unpack_mxfp4(const uint8_t* __
     const int64_t row = i / nb, b = i - row * nb;
     uint8_t* d = dst + i * 17;
     d[0] = scales[scale_at(row, b, kg)];
-    const uint8_t* c = codes + code_at(row, b, ks);
-    for (int k = 0; k < 16; k++) d[1 + k] = c[k];
+    const u32x4 v = *reinterpret_cast<const u32x4*>(codes + code_at(row, b, ks));
+    __builtin_memcpy(d + 1, &v, 16);
   }
 }
 
-template <int TYPE>
-__global__ __launch_bounds__(kPackThreads) void k_quantize_mxfp4(const typename Elem<TYPE>::T* __restrict__ X, int64_t stride,
+// Quantizer and its inverse: bound by the bytes that they move.  A wave takes S steps (512 of K, or
+// 128 where that would leave units idle) of a 16-row tile; the four lanes of a quad hold a block,
+// lane u the values 4u .. 4u + 3 and 16 + 4u .. 16 + 4u + 3, which are word u of its codes.  So a
+// load or store of floats covers 64-byte runs of 16 rows, and one of codes 256 bytes on end.
+template <typename T>
+__device__ __forceinline__ void load4(const T* p, bool vec, float (&f)[4]) {
+  T v[4];
+  if (vec) {
+    __builtin_memcpy(v, __builtin_assume_aligned(p, 4 * sizeof(T)), 4 * sizeof(T));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; j++) v[j] = p[j];
+  }
+#pragma unroll
+  for (int j = 0; j < 4; j++) f[j] = (float)v[j];
+}
+template <typename T>
+__device__ __forceinline__ void store4(T* p, bool vec, const float (&f)[4]) {
+  T v[4];
+#pragma unroll
+  for (int j = 0; j < 4; j++) v[j] = (T)f[j];
+  if (vec) {
+    __builtin_memcpy(__builtin_assume_aligned(p, 4 * sizeof(T)), v, 4 * sizeof(T));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; j++) p[j] = v[j];
+  }
+}
+template <int CTRL>
+__device__ __forceinline__ uint32_t quad_max(uint32_t x) {
+  const uint32_t y = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, 0xf, 0xf, true);
+  return x > y ? x : y;
+}
+
+template <int TYPE, int S>
+__global__ __launch_bounds__(kPackThreads) void k_quantize_mxfp4(const typename Elem<TYPE>::T* __restrict__ X, int64_t stride, int vec,
                                                                  uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
-                                                                 int64_t rows, int64_t nb, int64_t ks, int64_t kg, int64_t total) {
-  for (int64_t i = blockIdx.x * (int64_t)kPackThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kPackThreads) {
-    const int64_t row = i / (kg * 16), b = i - row * (kg * 16);
-    uint32_t byte = kOne;
-    u32x4 v{0, 0, 0, 0};
-    if (row < rows && b < nb) {
-      const auto* x = X + row * stride + b * 32;
-      float f[32], top = 0;
-      bool finite = true;
+                                                                 int64_t rows, int64_t nb, int64_t ks, int64_t kg, int64_t units) {
+  const int lane = threadIdx.x & 63, u = lane & 3, r = lane >> 2;
+  const int64_t per = kg * (4 / S);  // units of a row tile
+  for (int64_t i = blockIdx.x * (int64_t)kPackWaves + (threadIdx.x >> 6); i < units; i += (int64_t)gridDim.x * kPackWaves) {
+    const int64_t tile = i / per, s0 = (i - tile * per) * S, row = tile * 16 + r;
+    const auto* x = X + row * stride + 4 * u;
+    uint32_t word = 0;  // the scales of block u of each step
 #pragma unroll
-      for (int j = 0; j < 32; j++) {
-        f[j] = (float)x[j];
-        finite = finite && __builtin_isfinite(f[j]);
-        top = fmaxf(top, fabsf(f[j]));
-      }
-      // floor(log2 top) - 2 + 127 from the exponent field; e8m0 has nothing below 2^-127
-      const int field = (int)(__float_as_uint(top) >> 23);
-      byte = finite ? (field > 2 ? field - 2 : 0) : kNanScale;
-      if (finite) {
-        const float s = scale_of(byte);
+    for (int s = 0; s < S; s++) {
+      float f[4][2][4];
+      bool real[4];
 #pragma unroll
-        for (int j = 0; j < 4; j++) {
-          uint32_t w = 0;
-          w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, f[4 * j], f[4 * j + 16], s, 0);
-          w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, f[4 * j + 1], f[4 * j + 17], s, 1);
-          w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, f[4 * j + 2], f[4 * j + 18], s, 2);
-          v[j] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, f[4 * j + 3], f[4 * j + 19], s, 3);
+      for (int q = 0; q < 4; q++) {
+        const int64_t b = (s0 + s) * 4 + q;
+        real[q] = row < rows && b < nb;
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+          if (real[q]) {
+            load4(x + b * 32 + 16 * h, vec, f[q][h]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; j++) f[q][h][j] = 0;
+          }
         }
       }
+#pragma unroll
+      for (int q = 0; q < 4; q++) {
+        uint32_t top = 0;  // as bits: infinities above all numbers, NaN above those
+#pragma unroll
+        for (int h = 0; h < 2; h++)
+#pragma unroll
+          for (int j = 0; j < 4; j++) {
+            const uint32_t m = __float_as_uint(f[q][h][j]) & 0x7FFFFFFFu;
+            top = top > m ? top : m;
+          }
+        top = quad_max<0xB1>(top);
+        top = quad_max<0x4E>(top);
+        // floor(log2 top) - 2 + 127 from the exponent field; e8m0 has nothing below 2^-127
+        const uint32_t field = top >> 23, byte = !real[q] ? kOne : field == 255 ? kNanScale : field > 2 ? field - 2 : 0;
+        uint32_t c = 0;
+        if (field != 255) {
+          const float scale = scale_of(byte);
+          c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, f[q][0][0], f[q][1][0], scale, 0);
+          c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, f[q][0][1], f[q][1][1], scale, 1);
+          c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, f[q][0][2], f[q][1][2], scale, 2);
+          c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, f[q][0][3], f[q][1][3], scale, 3);
+        }
+        if (s0 + s < ks) *reinterpret_cast<uint32_t*>(codes + code_at(row, (s0 + s) * 4 + q, ks) + 4 * u) = c;
+        if (u == q) word |= byte << (8 * s);
+      }
     }
-    scales[scale_at(row, b, kg)] = (uint8_t)byte;
-    if (b < ks * 4) *reinterpret_cast<u32x4*>(codes + code_at(row, b, ks)) = v;
+    uint8_t* at = scales + scale_at(row, s0 * 4 + u, kg);
+    if constexpr (S == 4)
+      *reinterpret_cast<uint32_t*>(at) = word;
+    else
+      *at = (uint8_t)word;
   }
 }
 
 template <int TYPE>
 __global__ __launch_bounds__(kPackThreads) void k_dequantize_mxfp4(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
-                                                                   typename Elem<TYPE>::T* __restrict__ Y, int64_t stride,
-                                                                   int64_t nb, int64_t ks, int64_t kg, int64_t total) {
-  for (int64_t i = blockIdx.x * (int64_t)kPackThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kPackThreads) {
-    const int64_t row = i / nb, b = i - row * nb;
-    const float s = scale_of(scales[scale_at(row, b, kg)]);
-    const u32x4 v = *reinterpret_cast<const u32x4*>(codes + code_at(row, b, ks));
-    auto* y = Y + row * stride + b * 32;
+                                                                   typename Elem<TYPE>::T* __restrict__ Y, int64_t stride, int vec,
+                                                                   int64_t rows, int64_t nb, int64_t ks, int64_t kg, int64_t units) {
+  const int lane = threadIdx.x & 63, u = lane & 3, r = lane >> 2;
+  for (int64_t i = blockIdx.x * (int64_t)kPackWaves + (threadIdx.x >> 6); i < units; i += (int64_t)gridDim.x * kPackWaves) {
+    const int64_t tile = i / ks, s = i - tile * ks, row = tile * 16 + r;
+    uint32_t c[4], byte[4];
 #pragma unroll
-    for (int j = 0; j < 4; j++) {
-      const f32x2 p[4] = {pair_of<0>(v[j], 1.0f), pair_of<1>(v[j], 1.0f), pair_of<2>(v[j], 1.0f), pair_of<3>(v[j], 1.0f)};
+    for (int q = 0; q < 4; q++) {
+      c[q] = *reinterpret_cast<const uint32_t*>(codes + code_at(row, s * 4 + q, ks) + 4 * u);
+      byte[q] = scales[scale_at(row, s * 4 + q, kg)];
+    }
 #pragma unroll
-      for (int k = 0; k < 4; k++) {
-        y[4 * j + k] = (typename Elem<TYPE>::T)(p[k].x * s);
-        y[4 * j + k + 16] = (typename Elem<TYPE>::T)(p[k].y * s);
-      }
+    for (int q = 0; q < 4; q++) {
+      if (row >= rows || s * 4 + q >= nb) continue;
+      const float scale = scale_of(byte[q]);
+      const f32x2 p[4] = {pair_of<0>(c[q], 1.0f), pair_of<1>(c[q], 1.0f), pair_of<2>(c[q], 1.0f), pair_of<3>(c[q], 1.0f)};
+      auto* y = Y + row * stride + (s * 4 + q) * 32 + 4 * u;
+      const float lo[4] = {p[0].x * scale, p[1].x * scale, p[2].x * scale, p[3].x * scale};
+      const float hi[4] = {p[0].y * scale, p[1].y * scale, p[2].y * scale, p[3].y * scale};
+      store4(y, vec, lo);
+      store4(y + 16, vec, hi);
     }
   }
 }
@@ -126,14 +188,25 @@ int launch_unpack_mxfp4(const void* src, void* dst, int64_t rows, int64_t K, hip
   return launch_status();
 }
 
+static dim3 unit_grid(int64_t units) {
+  const int64_t g = (units + kPackWaves - 1) / kPackWaves;
+  return dim3((unsigned)(g < kPackGrid ? g : kPackGrid));
+}
+
 template <int TYPE>
 static int launch_quantize_as(const void* X, int64_t stride, void* packed, int64_t rows, int64_t K, hipStream_t s) {
   const MxLayout L = mx_layout(rows, K);
   uint8_t* codes = static_cast<uint8_t*>(packed);
-  const int64_t total = L.rt * kTileRows * L.kg * 16;
-  hipLaunchKernelGGL(k_quantize_mxfp4<TYPE>, pack_grid(total), dim3(kPackThreads), 0, s,
-                     static_cast<const typename Elem<TYPE>::T*>(X), stride, codes, codes + L.scales_off, rows, K / kQK, L.ks, L.kg,
-                     total);
+  const auto* x = static_cast<const typename Elem<TYPE>::T*>(X);
+  const int vec = stride % 4 == 0;
+  const int64_t units = L.rt * L.kg;
+  // four steps a wave where that makes eight waves a unit and more (17408 x 5120: 10880 waves)
+  if (units >= 2048)
+    hipLaunchKernelGGL((k_quantize_mxfp4<TYPE, 4>), unit_grid(units), dim3(kPackThreads), 0, s, x, stride, vec, codes,
+                       codes + L.scales_off, rows, K / kQK, L.ks, L.kg, units);
+  else
+    hipLaunchKernelGGL((k_quantize_mxfp4<TYPE, 1>), unit_grid(4 * units), dim3(kPackThreads), 0, s, x, stride, vec, codes,
+                       codes + L.scales_off, rows, K / kQK, L.ks, L.kg, 4 * units);
   return launch_status();
 }
 
@@ -147,9 +220,9 @@ template <int TYPE>
 static int launch_dequantize_as(const void* packed, void* Y, int64_t stride, int64_t rows, int64_t K, hipStream_t s) {
   const MxLayout L = mx_layout(rows, K);
   const uint8_t* codes = static_cast<const uint8_t*>(packed);
-  const int64_t total = rows * (K / kQK);
-  hipLaunchKernelGGL(k_dequantize_mxfp4<TYPE>, pack_grid(total), dim3(kPackThreads), 0, s, codes, codes + L.scales_off,
-                     static_cast<typename Elem<TYPE>::T*>(Y), stride, K / kQK, L.ks, L.kg, total);
+  const int64_t units = L.rt * L.ks;
+  hipLaunchKernelGGL(k_dequantize_mxfp4<TYPE>, unit_grid(units), dim3(kPackThreads), 0, s, codes, codes + L.scales_off,
+                     static_cast<typename Elem<TYPE>::T*>(Y), stride, (int)(stride % 4 == 0), rows, K / kQK, L.ks, L.kg, units);
   return launch_status();
 }
 
