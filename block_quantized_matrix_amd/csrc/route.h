@@ -9,6 +9,8 @@
 // then.  (exp in 64 bits runs at the rate of fp32 here; what binds the kernel is the selection.)
 #pragma once
 
+#include <type_traits>
+
 #include "mxfp4.h"
 
 namespace bqm {
@@ -24,7 +26,6 @@ struct RouteArgs {
   float* weights;
 };
 
-constexpr int kRouteWaves = 4;
 
 // f(value, the value of a lane that holds another part of the token's lanes), until all lanes have
 // taken in all: within quads, then mirrored halves and rows (each already alike inside), then
@@ -39,29 +40,16 @@ __device__ __forceinline__ double dpp(double x) {
   const uint32_t lo = dpp<CTRL>((int)(uint32_t)u), hi = dpp<CTRL>((int)(u >> 32));
   return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
-__device__ __forceinline__ void best2(double& v, int& i, double u, int j) {
-  if (u > v || (u == v && j < i)) {
-    v = u;
-    i = j;
-  }
+template <int CTRL>
+__device__ __forceinline__ float dpp(float x) {
+  return __builtin_bit_cast(float, dpp<CTRL>(__builtin_bit_cast(int, x)));
 }
-template <int G>
-__device__ __forceinline__ void best_of(double& v, int& i) {
-  best2(v, i, dpp<0xB1>(v), dpp<0xB1>(i));    // quad_perm 1 0 3 2
-  best2(v, i, dpp<0x4E>(v), dpp<0x4E>(i));    // quad_perm 2 3 0 1
-  best2(v, i, dpp<0x141>(v), dpp<0x141>(i));  // row_half_mirror
-  best2(v, i, dpp<0x140>(v), dpp<0x140>(i));  // row_mirror
-  if constexpr (G == 64) {
-    best2(v, i, __shfl_xor(v, 16, 64), __shfl_xor(i, 16, 64));
-    best2(v, i, __shfl_xor(v, 32, 64), __shfl_xor(i, 32, 64));
-  }
-}
-template <int G, typename F>
-__device__ __forceinline__ double reduce(double v, F&& f) {
-  v = f(v, dpp<0xB1>(v));
-  v = f(v, dpp<0x4E>(v));
-  v = f(v, dpp<0x141>(v));
-  v = f(v, dpp<0x140>(v));
+template <int G, typename T, typename F>
+__device__ __forceinline__ T reduce(T v, F&& f) {
+  v = f(v, dpp<0xB1>(v));   // quad_perm 1 0 3 2
+  v = f(v, dpp<0x4E>(v));   // quad_perm 2 3 0 1
+  v = f(v, dpp<0x141>(v));  // row_half_mirror
+  v = f(v, dpp<0x140>(v));  // row_mirror
   if constexpr (G == 64) {
     v = f(v, __shfl_xor(v, 16, 64));
     v = f(v, __shfl_xor(v, 32, 64));
@@ -69,13 +57,43 @@ __device__ __forceinline__ double reduce(double v, F&& f) {
   return v;
 }
 
-template <int TYPE, bool SIGMOID, int G, int V>
-__global__ __launch_bounds__(kRouteWaves * 64) void k_route(RouteArgs a) {
+// e^x by x = n ln 2 + r, |r| <= ln 2 / 2, and the Taylor series of e^r to r^13 / 13! (the next term
+// is below 2^-57): within two steps of 64 bits, in half the operations of the library's, which the
+// scores of 256 experts make felt.  x in [-1000, 709].
+__device__ __forceinline__ double exp64(double x) {
+  const double n = __builtin_rint(x * 0x1.71547652b82fep0);
+  double r = fma(n, -0x1.62e42fefa39efp-1, x);
+  r = fma(n, -0x1.abc9e3b39803fp-56, r);
+  double p = 1.0 / 6227020800.0;
+  constexpr double c[] = {1.0 / 479001600.0, 1.0 / 39916800.0, 1.0 / 3628800.0, 1.0 / 362880.0, 1.0 / 40320.0, 1.0 / 5040.0,
+                          1.0 / 720.0,       1.0 / 120.0,      1.0 / 24.0,      1.0 / 6.0,      0.5,           1.0,
+                          1.0};
+#pragma unroll
+  for (int k = 0; k < 13; k++) p = fma(p, r, c[k]);
+  return __builtin_ldexp(p, (int)n);
+}
+// 1 / x for x in [1, 2^1023]: the hardware's estimate and two Newton steps.
+__device__ __forceinline__ double rcp64(double x) {
+  double y = __builtin_amdgcn_rcp(x);
+  y = fma(fma(-x, y, 1.0), y, y);
+  return fma(fma(-x, y, 1.0), y, y);
+}
+// 1 / (1 + e^-x); where e^-x passes the range of 64 bits, 0.
+__device__ __forceinline__ double sigmoid64(float x) {
+  const double l = x;
+  const double s = rcp64(1.0 + exp64(fmin(fmax(-l, -709.0), 709.0)));
+  return l < -709.0 ? 0.0 : s;
+}
+
+// BIAS: the order is that of scores with their bias, 64 bits; without it that of the logits as they
+// are, fp32.
+template <int TYPE, bool SIGMOID, bool BIAS, int G, int V, int WAVES>
+__global__ __launch_bounds__(WAVES * 64) void k_route(RouteArgs a) {
   typedef typename mx::Elem<TYPE>::T Elem;
-  constexpr int kTokens = kRouteWaves * 64 / G;  // of a workgroup
+  typedef std::conditional_t<BIAS, double, float> Key;
+  constexpr int kTokens = WAVES * 64 / G;  // of a workgroup
   constexpr int kVec = 16 / sizeof(Elem);
-  constexpr int kHeld = V * G <= 1024 ? V * G : 1;  // values that fit LDS beside one another
-  __shared__ double val_lds[kTokens * (V * G <= 1024 ? kHeld : 1)];
+  __shared__ double val_lds[kTokens][V * G];  // values, or each lane's two largest
   __shared__ double grp_lds[kTokens][BQM_ROUTE_MAX_GROUPS];
   const int lane = threadIdx.x % G, at = threadIdx.x / G;
   const int64_t t = (int64_t)blockIdx.x * kTokens + at;
@@ -98,54 +116,71 @@ __global__ __launch_bounds__(kRouteWaves * 64) void k_route(RouteArgs a) {
   }
   float bias[V];
 #pragma unroll
-  for (int v = 0; v < V; v++) bias[v] = a.bias && e0 + v < a.E ? a.bias[e0 + v] : 0.0f;
+  for (int v = 0; v < V; v++) bias[v] = BIAS && e0 + v < a.E ? a.bias[e0 + v] : 0.0f;
   // the row's maximum and whether anything in it is no number
-  double top = -inf, bad = 0;
+  float top = -__builtin_inff(), bad = 0;
 #pragma unroll
   for (int v = 0; v < V; v++) {
-    top = x[v] > top ? (double)x[v] : top;
+    top = x[v] > top ? x[v] : top;
     if (x[v] != x[v] || bias[v] != bias[v] || (!SIGMOID && x[v] == __builtin_inff())) bad = 1;
   }
-  bad = reduce<G>(bad, [](double p, double q) { return p > q ? p : q; });
-  const bool sums = a.n_group > 1 && a.group_top == 2, scored = a.bias || sums;
-  double total = 1;
-  if (!SIGMOID) {
-    top = reduce<G>(top, [](double p, double q) { return p > q ? p : q; });
-    if (scored || !a.renorm) {
+  bad = reduce<G>(bad, [](float p, float q) { return p > q ? p : q; });
+  const bool sums = a.n_group > 1 && a.group_top == 2, scored = BIAS || sums;
+  double total = 1, rtotal = 1;
+  if (!SIGMOID) top = reduce<G>(top, [](float p, float q) { return p > q ? p : q; });
+  // e^(x - top), 0 where that is below the range
+  auto power = [&](float f) {
+    const double d = (double)f - (double)top;
+    return d < -746.0 ? 0.0 : exp64(fmax(d, -746.0));
+  };
+  double score[V];
+  if (scored || (!SIGMOID && !a.renorm)) {
+#pragma unroll
+    for (int v = 0; v < V; v++) score[v] = x[v] == -__builtin_inff() ? 0.0 : SIGMOID ? sigmoid64(x[v]) : power(x[v]);
+    if (!SIGMOID) {
       total = 0;
 #pragma unroll
-      for (int v = 0; v < V; v++) total += x[v] == -__builtin_inff() ? 0.0 : exp((double)x[v] - top);
+      for (int v = 0; v < V; v++) total += score[v];
       total = reduce<G>(total, [](double p, double q) { return p + q; });
+      rtotal = total > 0 ? rcp64(total) : 0.0;  // 0 only where every expert is masked
+#pragma unroll
+      for (int v = 0; v < V; v++) score[v] *= rtotal;
     }
   }
-  auto score = [&](float f) { return SIGMOID ? 1.0 / (1.0 + exp(-(double)f)) : exp((double)f - top) / total; };
-  double val[V];
+  // no NaN among the keys: it would be neither above nor below the others (its token is `bad`)
+  Key key[V];
 #pragma unroll
   for (int v = 0; v < V; v++) {
-    const double s = scored ? score(x[v]) : (double)x[v];
-    val[v] = x[v] == -__builtin_inff() ? -inf : s + (double)bias[v];
+    if constexpr (BIAS) {
+      const double k = score[v] + (double)bias[v];
+      key[v] = x[v] > -__builtin_inff() && k > -inf ? k : -inf;
+    } else {
+      key[v] = x[v] > -__builtin_inff() ? x[v] : -__builtin_inff();
+    }
   }
   if (a.n_group > 1) {
     const int size = a.E / a.n_group;
-    double* held = val_lds + at * kHeld;
-    if constexpr (V * G <= 1024) {
+    double v1 = -inf, v2 = -inf;
+    auto take = [&](double v) {
+      v2 = v > v1 ? v1 : v > v2 ? v : v2;
+      v1 = v > v1 ? v : v1;
+    };
+    auto value = [&](int v) { return BIAS ? (double)key[v] : x[v] == -__builtin_inff() ? -inf : sums ? score[v] : (double)x[v]; };
+    const bool whole = size % V == 0 && V > 1;  // a lane's experts are of one group
+    if (whole) {
 #pragma unroll
-      for (int v = 0; v < V; v++) held[e0 + v] = val[v];
+      for (int v = 0; v < V; v++) take(value(v));
+      val_lds[at][2 * lane] = v1;
+      val_lds[at][2 * lane + 1] = v2;
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; v++) val_lds[at][e0 + v] = value(v);
     }
     __syncthreads();
+    const int each = whole ? size / V * 2 : size;
     for (int g = lane; g < a.n_group; g += G) {
-      double v1 = -inf, v2 = -inf;
-      for (int e = g * size; e < (g + 1) * size; e++) {
-        double v;
-        if constexpr (V * G <= 1024) {
-          v = held[e];
-        } else {
-          const float f = (float)l[e];
-          v = f == -__builtin_inff() ? -inf : (scored ? score(f) : (double)f) + (a.bias ? (double)a.bias[e] : 0.0);
-        }
-        v2 = v > v1 ? v1 : v > v2 ? v : v2;
-        v1 = v > v1 ? v : v1;
-      }
+      v1 = v2 = -inf;
+      for (int e = g * each; e < (g + 1) * each; e++) take(val_lds[at][e]);
       grp_lds[at][g] = a.group_top == 2 && v2 != -inf ? v1 + v2 : v1;
     }
     __syncthreads();
@@ -165,8 +200,7 @@ __global__ __launch_bounds__(kRouteWaves * 64) void k_route(RouteArgs a) {
     int g = e0 < a.E ? e0 / size : 0, rest = e0 - g * size;
 #pragma unroll
     for (int v = 0; v < V; v++) {
-      const double own = a.bias ? val[v] : (double)x[v];  // group sums were of scores, the order is the logits'
-      val[v] = open >> (g & 63) & 1 ? own : -inf;
+      key[v] = open >> (g & 63) & 1 ? key[v] : (Key)-inf;
       const bool turn = ++rest == size;
       g += turn;
       rest = turn ? 0 : rest;
@@ -178,26 +212,25 @@ __global__ __launch_bounds__(kRouteWaves * 64) void k_route(RouteArgs a) {
 #pragma unroll
   for (int k = 0; k < kKept; k++) kept[k] = -1;
   for (int s = 0; s < a.top_k; s++) {
-    double best = -inf;
+    Key best = key[0];
+#pragma unroll
+    for (int v = 1; v < V; v++) best = key[v] > best ? key[v] : best;
+    best = reduce<G>(best, [](Key p, Key q) { return p > q ? p : q; });
     int i = 1 << 30;
 #pragma unroll
-    for (int v = 0; v < V; v++)
-      if (val[v] > best) {
-        best = val[v];
-        i = e0 + v;
-      }
-    best_of<G>(best, i);
+    for (int v = V - 1; v >= 0; v--) i = key[v] == best ? e0 + v : i;
+    i = reduce<G>(i, [](int p, int q) { return p < q ? p : q; });
 #pragma unroll
-    for (int v = 0; v < V; v++)
-      if (e0 + v == i) val[v] = -inf;
+    for (int v = 0; v < V; v++) key[v] = e0 + v == i ? (Key)-inf : key[v];
 #pragma unroll
     for (int k = 0; k < kKept; k++)
-      if (s == k * G + lane) kept[k] = best == -inf ? -1 : i;
+      if (s == k * G + lane) kept[k] = best > (Key)-inf && i < a.E ? i : -1;
   }
   double w[kKept], chosen = 0;
 #pragma unroll
   for (int k = 0; k < kKept; k++) {
-    w[k] = kept[k] >= 0 ? score((float)l[kept[k]]) : 0.0;
+    const float f = kept[k] >= 0 ? (float)l[kept[k]] : 0.0f;
+    w[k] = kept[k] < 0 ? 0.0 : SIGMOID ? sigmoid64(f) : power(f) * rtotal;
     chosen += w[k];
   }
   if (a.renorm) chosen = reduce<G>(chosen, [](double p, double q) { return p + q; });
@@ -219,9 +252,10 @@ __global__ __launch_bounds__(kRouteWaves * 64) void k_route(RouteArgs a) {
 
 template <int TYPE, int G, int V>
 int launch_route_as(int score, const RouteArgs& a, hipStream_t s) {
-  constexpr int kTokens = kRouteWaves * 64 / G;
-  hipLaunchKernelGGL(score == BQM_SIGMOID ? (k_route<TYPE, true, G, V>) : (k_route<TYPE, false, G, V>),
-                     dim3((unsigned)((a.T + kTokens - 1) / kTokens)), dim3(kRouteWaves * 64), 0, s, a);
+  constexpr int kWaves = G * V > 1024 ? 1 : 4, kTokens = kWaves * 64 / G;
+  auto* k = score == BQM_SIGMOID ? (a.bias ? k_route<TYPE, true, true, G, V, kWaves> : k_route<TYPE, true, false, G, V, kWaves>)
+                                 : (a.bias ? k_route<TYPE, false, true, G, V, kWaves> : k_route<TYPE, false, false, G, V, kWaves>);
+  hipLaunchKernelGGL(k, dim3((unsigned)((a.T + kTokens - 1) / kTokens)), dim3(kWaves * 64), 0, s, a);
   return launch_status();
 }
 
