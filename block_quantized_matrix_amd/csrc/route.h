@@ -3,10 +3,17 @@
 // A token's E values lie in the registers of G lanes, V neighbouring experts a lane: sixteen lanes a
 // token (four tokens a wave) where there are tokens enough to fill the chip, since a reduction over
 // sixteen lanes takes four DPP steps and serves four tokens; all 64 lanes otherwise.  Each of the
-// top_k rounds takes the largest value and, of equal ones, the lowest index, first over a
-// lane's registers, then over its lanes.  Values are 64 bits wide: between neighbours in the order
-// of the real numbers an id hangs on the last bits of a score, and fp32 scores would swap them now and
-// then.  (exp in 64 bits runs at the rate of fp32 here; what binds the kernel is the selection.)
+// top_k rounds takes the largest value and, of equal ones, the lowest index.
+//
+// Between neighbours in the order of the real numbers an id hangs on the last bits of a score: fp32
+// scores would swap them now and then.  So the order is that of 64-bit scores, but up to 256 experts
+// the rounds go by fp32 keys, whose last bits hold the place in the lane, and take two experts
+// more than asked for; these few are then put in order by their 64-bit scores, which the
+// weights need anyway.  What the keys leave open (a third candidate, or a group, nearer than the
+// keys are exact; a softmax with a bias, whose 64-bit scores need all experts) the wave selects again
+// in 64 bits.  16-bit logits without a bias leave the last bits free: their keys are exact.  The
+// rounds' vector work binds the kernel.  Measured (16384 tokens, 256 experts, top-8): without a bias 7.3
+// us, sigmoid with a bias 16 us, in groups 22 us; with 64 bits throughout 10, 22 and 25.
 #pragma once
 
 #include <type_traits>
@@ -94,7 +101,7 @@ __global__ __launch_bounds__(WAVES * 64) void k_route(RouteArgs a) {
   constexpr int kTokens = WAVES * 64 / G;  // of a workgroup
   constexpr int kVec = 16 / sizeof(Elem);
   __shared__ double val_lds[kTokens][V * G];  // values, or each lane's two largest
-  __shared__ double grp_lds[kTokens][BQM_ROUTE_MAX_GROUPS];
+  __shared__ double grp_lds[kTokens][BQM_ROUTE_MAX_GROUPS];  // and the candidates' ids after that
   const int lane = threadIdx.x % G, at = threadIdx.x / G;
   const int64_t t = (int64_t)blockIdx.x * kTokens + at;
   const int64_t row = t < a.T ? t : a.T - 1;  // lanes past the last token repeat it and write nothing
@@ -126,117 +133,292 @@ __global__ __launch_bounds__(WAVES * 64) void k_route(RouteArgs a) {
   }
   bad = reduce<G>(bad, [](float p, float q) { return p > q ? p : q; });
   const bool sums = a.n_group > 1 && a.group_top == 2, scored = BIAS || sums;
-  double total = 1, rtotal = 1;
   if (!SIGMOID) top = reduce<G>(top, [](float p, float q) { return p > q ? p : q; });
+  // lane s % G keeps slot s, and its place in the order
+  constexpr int kKept = (BQM_QMV_ID_MAX_TOPK + 2 + G - 1) / G;
+  int kept[kKept], place[kKept];
+  double w[kKept];
+  auto keep = [&](int s, int id) {
+#pragma unroll
+    for (int k = 0; k < kKept; k++)
+      if (s == k * G + lane) kept[k] = id;
+  };
+  // The groups that stay open, one bit each, from the lanes' values of type T; near: whether two
+  // groups are within `margin` (negative: never).
+  const int size = a.n_group > 1 ? a.E / a.n_group : 1;
+  const bool whole = size % V == 0 && V > 1;  // a lane's experts are of one group
+  auto open_groups = [&](auto zero, auto&& value, decltype(zero) margin, bool& near) {
+    typedef decltype(zero) T;
+    T* vals = reinterpret_cast<T*>(val_lds[at]);
+    T* sums2 = reinterpret_cast<T*>(grp_lds[at]);
+    T v1 = (T)-inf, v2 = (T)-inf;
+    auto take = [&](T v) {  // the largest and the second largest so far
+      if constexpr (sizeof(T) == 4)
+        v2 = __builtin_amdgcn_fmed3f(v1, v2, v);
+      else
+        v2 = v > v1 ? v1 : v > v2 ? v : v2;
+      v1 = v > v1 ? v : v1;
+    };
+    if (whole) {
+#pragma unroll
+      for (int v = 0; v < V; v++) take(value(v));
+      vals[2 * lane] = v1;
+      vals[2 * lane + 1] = v2;
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; v++) vals[e0 + v] = value(v);
+    }
+    mx::wave_turn();  // a token's lanes are of one wave
+    const int each = whole ? size / V * 2 : size;
+    for (int g = lane; g < a.n_group; g += G) {
+      v1 = v2 = (T)-inf;
+      for (int e = g * each; e < (g + 1) * each; e++) take(vals[e]);
+      sums2[g] = a.group_top == 2 && v2 != (T)-inf ? v1 + v2 : v1;
+    }
+    mx::wave_turn();
+    uint64_t open = 0;
+    bool close = false;
+    for (int g = 0; g < a.n_group; g += G) {
+      const int h = g + lane;
+      int before = 0;
+      if (h < a.n_group) {
+        const T w = sums2[h];
+        for (int k = 0; k < a.n_group; k++) {
+          const T u = sums2[k];
+          before += u > w || (u == w && k < h);
+          close = close || (k != h && u - w <= margin && w - u <= margin);
+        }
+      }
+      const uint64_t b = __ballot(h < a.n_group && before < a.topk_group);
+      open |= (G == 64 ? b : b >> (threadIdx.x % 64 / G * G) & ((1ull << (G % 64)) - 1)) << g;
+    }
+    mx::wave_turn();  // the next pass writes there again
+    near = near || close;
+    return open;
+  };
+  // f(v, whether the group of expert e0 + v is open)
+  auto for_open = [&](uint64_t open, auto&& f) {
+    int g = e0 < a.E ? e0 / size : 0, rest = e0 - g * size;
+    if (whole) {
+      const bool in = open >> (g & 63) & 1;
+#pragma unroll
+      for (int v = 0; v < V; v++) f(v, in);
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; v++) {
+        f(v, open >> (g & 63) & 1);
+        const bool turn = ++rest == size;
+        g += turn;
+        rest = turn ? 0 : rest;
+      }
+    }
+  };
   // e^(x - top), 0 where that is below the range
   auto power = [&](float f) {
     const double d = (double)f - (double)top;
     return d < -746.0 ? 0.0 : exp64(fmax(d, -746.0));
   };
-  double score[V];
-  if (scored || (!SIGMOID && !a.renorm)) {
+  double rtotal = 1;  // 1 / the softmax's sum, where that counts
+  auto scores64 = [&](double (&score)[V]) {
+    double total = 0;
 #pragma unroll
-    for (int v = 0; v < V; v++) score[v] = x[v] == -__builtin_inff() ? 0.0 : SIGMOID ? sigmoid64(x[v]) : power(x[v]);
-    if (!SIGMOID) {
-      total = 0;
-#pragma unroll
-      for (int v = 0; v < V; v++) total += score[v];
+    for (int v = 0; v < V; v++) {
+      score[v] = x[v] == -__builtin_inff() ? 0.0 : SIGMOID ? sigmoid64(x[v]) : power(x[v]);
+      total += score[v];
+    }
+    if constexpr (!SIGMOID) {
       total = reduce<G>(total, [](double p, double q) { return p + q; });
       rtotal = total > 0 ? rcp64(total) : 0.0;  // 0 only where every expert is masked
 #pragma unroll
       for (int v = 0; v < V; v++) score[v] *= rtotal;
     }
-  }
-  // no NaN among the keys: it would be neither above nor below the others (its token is `bad`)
-  Key key[V];
-#pragma unroll
-  for (int v = 0; v < V; v++) {
-    if constexpr (BIAS) {
-      const double k = score[v] + (double)bias[v];
-      key[v] = x[v] > -__builtin_inff() && k > -inf ? k : -inf;
-    } else {
-      key[v] = x[v] > -__builtin_inff() ? x[v] : -__builtin_inff();
-    }
-  }
-  if (a.n_group > 1) {
-    const int size = a.E / a.n_group;
-    double v1 = -inf, v2 = -inf;
-    auto take = [&](double v) {
-      v2 = v > v1 ? v1 : v > v2 ? v : v2;
-      v1 = v > v1 ? v : v1;
-    };
-    auto value = [&](int v) { return BIAS ? (double)key[v] : x[v] == -__builtin_inff() ? -inf : sums ? score[v] : (double)x[v]; };
-    const bool whole = size % V == 0 && V > 1;  // a lane's experts are of one group
-    if (whole) {
-#pragma unroll
-      for (int v = 0; v < V; v++) take(value(v));
-      val_lds[at][2 * lane] = v1;
-      val_lds[at][2 * lane + 1] = v2;
-    } else {
-#pragma unroll
-      for (int v = 0; v < V; v++) val_lds[at][e0 + v] = value(v);
-    }
-    __syncthreads();
-    const int each = whole ? size / V * 2 : size;
-    for (int g = lane; g < a.n_group; g += G) {
-      v1 = v2 = -inf;
-      for (int e = g * each; e < (g + 1) * each; e++) take(val_lds[at][e]);
-      grp_lds[at][g] = a.group_top == 2 && v2 != -inf ? v1 + v2 : v1;
-    }
-    __syncthreads();
-    // groups that stay open, one bit each
-    uint64_t open = 0;
-    for (int g = 0; g < a.n_group; g += G) {
-      const int h = g + lane;
-      int before = 0;
-      if (h < a.n_group)
-        for (int k = 0; k < a.n_group; k++) {
-          const double u = grp_lds[at][k], w = grp_lds[at][h];
-          before += u > w || (u == w && k < h);
-        }
-      const uint64_t b = __ballot(h < a.n_group && before < a.topk_group);
-      open |= (G == 64 ? b : b >> (threadIdx.x % 64 / G * G) & ((1ull << (G % 64)) - 1)) << g;
-    }
-    int g = e0 < a.E ? e0 / size : 0, rest = e0 - g * size;
-#pragma unroll
-    for (int v = 0; v < V; v++) {
-      key[v] = open >> (g & 63) & 1 ? key[v] : (Key)-inf;
-      const bool turn = ++rest == size;
-      g += turn;
-      rest = turn ? 0 : rest;
-    }
-  }
-  // the rounds; lane s % G keeps slot s
-  constexpr int kKept = BQM_QMV_ID_MAX_TOPK / G > 0 ? BQM_QMV_ID_MAX_TOPK / G : 1;
-  int kept[kKept];
-#pragma unroll
-  for (int k = 0; k < kKept; k++) kept[k] = -1;
-  for (int s = 0; s < a.top_k; s++) {
-    Key best = key[0];
-#pragma unroll
-    for (int v = 1; v < V; v++) best = key[v] > best ? key[v] : best;
-    best = reduce<G>(best, [](Key p, Key q) { return p > q ? p : q; });
-    int i = 1 << 30;
-#pragma unroll
-    for (int v = V - 1; v >= 0; v--) i = key[v] == best ? e0 + v : i;
-    i = reduce<G>(i, [](int p, int q) { return p < q ? p : q; });
-#pragma unroll
-    for (int v = 0; v < V; v++) key[v] = e0 + v == i ? (Key)-inf : key[v];
-#pragma unroll
-    for (int k = 0; k < kKept; k++)
-      if (s == k * G + lane) kept[k] = best > (Key)-inf && i < a.E ? i : -1;
-  }
-  double w[kKept], chosen = 0;
+  };
 #pragma unroll
   for (int k = 0; k < kKept; k++) {
-    const float f = kept[k] >= 0 ? (float)l[kept[k]] : 0.0f;
-    w[k] = kept[k] < 0 ? 0.0 : SIGMOID ? sigmoid64(f) : power(f) * rtotal;
-    chosen += w[k];
+    kept[k] = -1;
+    place[k] = k * G + lane;
+  }
+  bool again = true, weighed = false;
+  // (one token's latency is less without it)
+  if constexpr (V * G <= 256 && (G == 16 || (!BIAS && sizeof(Elem) == 2))) {
+    // The fp32 pass.  A sigmoid is within kOff of the real one: the product x log2 e and v_exp_f32 move
+    // e^-x by 1.25 |x| + 2 steps of 2^-24 of it, which s (1 - s) |x| <= 0.23 makes 0.8 steps of 1; the
+    // sum, v_rcp_f32 add 3: below 2^-22.  A softmax's terms and its sum of 256 (16 in turn, then a
+    // tree) and its reciprocal: 27 steps of 2^-24, below 2^-19.
+    constexpr float kOff = SIGMOID ? 0x1p-22f : 0x1p-19f, kLog2e = 0x1.715476p+0f;
+    again = false;
+    float score[V], total = 0;
+    if (scored) {
+#pragma unroll
+      for (int v = 0; v < V; v++) {
+        score[v] = SIGMOID ? __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-x[v] * kLog2e))
+                   : x[v] > -__builtin_inff() ? __builtin_amdgcn_exp2f((x[v] - top) * kLog2e)
+                                              : 0.0f;
+        total += score[v];
+      }
+      if (!SIGMOID) {
+        total = __builtin_amdgcn_rcpf(reduce<G>(total, [](float p, float q) { return p + q; }));
+#pragma unroll
+        for (int v = 0; v < V; v++) score[v] *= total;
+      }
+    }
+    float val[V];
+#pragma unroll
+    for (int v = 0; v < V; v++) {
+      const float k = BIAS ? score[v] + bias[v] : x[v];
+      val[v] = x[v] > -__builtin_inff() && k > -__builtin_inff() ? k : -__builtin_inff();  // and no NaN
+    }
+    if (a.n_group > 1) {
+      // each of the two values of a sum is kOff off and rounded, the sum too; logits are exact
+      float most = 0;
+#pragma unroll
+      for (int v = 0; v < V; v++) most = BIAS && __builtin_fabsf(bias[v]) > most ? __builtin_fabsf(bias[v]) : most;
+      most = reduce<G>(most, [](float p, float q) { return p > q ? p : q; });
+      const float margin = scored ? 4.0f * (kOff + 0x1p-22f * (1 + most)) : -1.0f;
+      bool near = false;
+      uint64_t open = open_groups(
+          0.0f, [&](int v) { return !BIAS && sums && val[v] > -__builtin_inff() ? score[v] : val[v]; }, margin, near);
+      if (__any(near && bad == 0)) {  // groups nearer than fp32 tells: by their 64-bit values
+        double exact[V];
+        scores64(exact);
+        open = open_groups(0.0, [&](int v) { return val[v] == -__builtin_inff() ? -inf : BIAS ? exact[v] + (double)bias[v] : exact[v]; }, -1.0,
+                           near);
+      }
+      for_open(open, [&](int v, bool in) { val[v] = in ? val[v] : -__builtin_inff(); });
+    }
+    // Keys: the value's bits in the order of unsigned numbers, the last ones V - 1 - v; where the
+    // value leaves thirteen of them free, 255 - e, which orders equal values of all lanes.
+    constexpr bool kExact = !BIAS && sizeof(Elem) == 2;
+    constexpr uint32_t kLast = kExact ? 255 : V - 1;
+    constexpr uint32_t kNone = 0x007FFFFFu;  // of -infinity
+    uint32_t key[V];
+#pragma unroll
+    for (int v = 0; v < V; v++) {
+      const uint32_t u = __float_as_uint(val[v] + 0.0f);  // -0 is 0
+      key[v] = ((u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u)) & ~kLast) | (kLast - (kExact ? e0 + v : v));
+    }
+    const int rounds = a.top_k + (kExact ? 0 : 2);
+    // Two keys are as far apart as the real values but for kOff each (with a bias), a rounding each and
+    // the last bits, which take less than V steps of 2^-23 from either.
+    auto apart = [&](float f, float g) {
+      const float span = __builtin_fabsf(f) > __builtin_fabsf(g) ? __builtin_fabsf(f) : __builtin_fabsf(g);
+      return f - g > (BIAS ? 2 * kOff : 0.0f) + span * ((V + 1) * 0x1p-23f);
+    };
+    constexpr bool kRank = !kExact && (SIGMOID || !BIAS);  // 64-bit values of a few experts alone
+    float last = 0;
+    for (int s = 0; s < rounds; s++) {
+      uint32_t mine = key[0];
+#pragma unroll
+      for (int v = 1; v < V; v++) mine = key[v] > mine ? key[v] : mine;
+      const uint32_t best = (uint32_t)reduce<G>((int)(mine ^ 0x80000000u), [](int p, int q) { return p > q ? p : q; }) ^ 0x80000000u;
+      int i = (int)(255 - (best & 255));
+      if constexpr (!kExact) {
+        i = mine == best ? e0 + (int)(kLast - (mine & kLast)) : 1 << 30;
+        i = reduce<G>(i, [](int p, int q) { return p < q ? p : q; });
+      }
+      const bool none = (best | kLast) <= (kNone | kLast);
+#pragma unroll
+      for (int v = 0; v < V; v++) key[v] = i - e0 == v ? 0u : key[v];
+      if constexpr (!kExact) {
+        const uint32_t o = best & ~kLast;
+        const float f = __uint_as_float(o ^ (o >> 31 ? 0x80000000u : 0xFFFFFFFFu));
+        if (kRank) {  // the last candidate has to lie below the last wanted
+          if (s == a.top_k - 1) last = f;
+          if (s == rounds - 1 && !none && !apart(last, f)) again = true;
+        } else {      // each below the one before it
+          if (s > 0 && s <= a.top_k && !none && !apart(last, f)) again = true;
+          last = f;
+        }
+      }
+      if (kRank || s < a.top_k) keep(s, !none && i < a.E ? i : -1);
+    }
+    if constexpr (kRank) {
+      weighed = true;
+      int* ids = reinterpret_cast<int*>(grp_lds[at]);
+      static_assert(sizeof(grp_lds[0]) >= (BQM_QMV_ID_MAX_TOPK + 2) * sizeof(int) && V * G >= BQM_QMV_ID_MAX_TOPK + 2, "room");
+      double val[kKept];
+#pragma unroll
+      for (int k = 0; k < kKept; k++) {
+        w[k] = 0;
+        val[k] = -inf;
+        if (k * G >= rounds) continue;
+        const float f = kept[k] >= 0 ? (float)l[kept[k]] : 0.0f;
+        w[k] = kept[k] < 0 ? 0.0 : SIGMOID ? sigmoid64(f) : 0.0;
+        val[k] = kept[k] < 0 ? -inf : BIAS ? w[k] + (double)a.bias[kept[k]] : (double)f;
+        if (place[k] < rounds) {
+          val_lds[at][place[k]] = val[k];
+          ids[place[k]] = kept[k];
+        }
+      }
+      mx::wave_turn();
+#pragma unroll
+      for (int k = 0; k < kKept; k++) place[k] = kept[k] < 0 ? k * G + lane : 0;
+      for (int s = 0; s < rounds; s++) {
+        const double u = val_lds[at][s];
+        const int j = ids[s];
+#pragma unroll
+        for (int k = 0; k < kKept; k++)
+          if (k * G < rounds) place[k] += kept[k] >= 0 && j >= 0 && (u > val[k] || (u == val[k] && j < kept[k]));
+      }
+      mx::wave_turn();
+    }
+    again = __any(again && bad == 0);
+  }
+  double score[V];
+  if ((again && scored) || (!SIGMOID && !a.renorm)) scores64(score);
+  if (again) {
+    weighed = false;
+#pragma unroll
+    for (int k = 0; k < kKept; k++) {
+      kept[k] = -1;
+      place[k] = k * G + lane;
+    }
+    // no NaN among the keys: it would be neither above nor below the others (its token is `bad`)
+    Key key[V];
+#pragma unroll
+    for (int v = 0; v < V; v++) {
+      if constexpr (BIAS) {
+        const double k = score[v] + (double)bias[v];
+        key[v] = x[v] > -__builtin_inff() && k > -inf ? k : -inf;
+      } else {
+        key[v] = x[v] > -__builtin_inff() ? x[v] : -__builtin_inff();
+      }
+    }
+    if (a.n_group > 1) {
+      bool near = false;
+      const uint64_t open = open_groups(
+          0.0, [&](int v) { return BIAS ? (double)key[v] : key[v] == (Key)-inf ? -inf : sums ? score[v] : (double)key[v]; }, -1.0, near);
+      for_open(open, [&](int v, bool in) { key[v] = in ? key[v] : (Key)-inf; });
+    }
+    for (int s = 0; s < a.top_k; s++) {
+      Key best = key[0];
+#pragma unroll
+      for (int v = 1; v < V; v++) best = key[v] > best ? key[v] : best;
+      best = reduce<G>(best, [](Key p, Key q) { return p > q ? p : q; });
+      int i = 1 << 30;
+#pragma unroll
+      for (int v = V - 1; v >= 0; v--) i = key[v] == best ? e0 + v : i;
+      i = reduce<G>(i, [](int p, int q) { return p < q ? p : q; });
+#pragma unroll
+      for (int v = 0; v < V; v++) key[v] = e0 + v == i ? (Key)-inf : key[v];
+      keep(s, best > (Key)-inf && i < a.E ? i : -1);
+    }
+  }
+  double chosen = 0;
+#pragma unroll
+  for (int k = 0; k < kKept; k++) {
+    if (!(weighed && SIGMOID)) {
+      w[k] = 0;
+      if (k * G >= a.top_k + 2) continue;
+      const float f = kept[k] >= 0 ? (float)l[kept[k]] : 0.0f;
+      w[k] = kept[k] < 0 ? 0.0 : SIGMOID ? sigmoid64(f) : power(f) * rtotal;
+    }
+    chosen += place[k] < a.top_k ? w[k] : 0.0;
   }
   if (a.renorm) chosen = reduce<G>(chosen, [](double p, double q) { return p + q; });
 #pragma unroll
   for (int k = 0; k < kKept; k++) {
-    const int s = k * G + lane;
+    const int s = place[k];
     if (t >= a.T || s >= a.top_k) continue;
     if (a.renorm) w[k] = chosen == 0 ? 0.0 : w[k] / chosen;
     float f = (float)(w[k] * (double)a.scale);
@@ -259,6 +441,8 @@ int launch_route_as(int score, const RouteArgs& a, hipStream_t s) {
   return launch_status();
 }
 
+// Sixteen lanes a token from 1024 tokens on (16384 x 128, top-8: 5.7 us), where that fills the chip's
+// units; below, 64 lanes a token end sooner (512 x 256 with a bias in groups: 9 us).
 template <int TYPE>
 int launch_route_type(int score, const RouteArgs& a, hipStream_t s) {
   if (a.E <= 256 && a.T >= 1024)

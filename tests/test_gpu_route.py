@@ -118,6 +118,34 @@ def test_masks_and_specials(score):
         check(x.to(dtype), bias, score, 4, 2, 2, 6, True, 1.0)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("E,n_group,topk_group,top_k", [(60, 1, 1, 8), (64, 4, 2, 6), (128, 1, 1, 8), (96, 3, 2, 30), (250, 5, 2, 8),
+                                                        (256, 8, 4, 8), (256, 64, 9, 32)])
+def test_long_prompts(E, n_group, topk_group, top_k, dtype, score):
+    """Prompts take fewer lanes a token and select by 32-bit keys first: random logits, ties, steps in the last bit, values
+    that only 64 bits tell apart, masks and NaN, all in one batch."""
+    say("route long", E, n_group, topk_group, top_k, dtype, score)
+    T, g, t = 1101, np.random.default_rng(E), TYPES[dtype]
+    l = gen.normal((T, E), ("route-long", E), device=DEV) * 1.5
+    l[300:400] = torch.from_numpy(g.integers(-2, 3, (100, E)).astype(np.float32)).to(DEV)          # ties
+    l[400:500] = torch.from_numpy(1 + g.integers(0, 200, (100, E)) * 2.0 ** -23).float().to(DEV)   # neighbours
+    l[500:520] = 0
+    l[520:540, ::3] = float("-inf")
+    l[540:550, 2:] = float("-inf")
+    l[550] = float("-inf")
+    l[551, 5], l[552, 7], l[553, 1] = float("nan"), float("inf"), torch.finfo(torch.float32).min
+    l = l.to(t)
+    random = gen.normal((E,), ("route-long-b", E), std=0.05, device=DEV)
+    steps = torch.from_numpy((g.integers(0, 50, E) * 2.0 ** -30).astype(np.float32)).to(DEV)
+    wide = random.clone()
+    wide[::7] *= 1e6
+    for bias in (None, random, torch.zeros_like(random), steps, wide):
+        for group_top in (1, 2) if n_group > 1 else (1,):
+            check(l, bias, score, n_group, topk_group, group_top, top_k, True, 1.0)
+    check(l, random, score, n_group, topk_group, 1, min(top_k, 3), False, 2.5)
+
+
 def test_strides_and_empty():
     say("route strides")
     for dtype in TYPES.values():
