@@ -302,30 +302,21 @@ __global__ __launch_bounds__(WN* WM* KS * 64) __attribute__((amdgpu_waves_per_eu
   __shared__ int wsum[NT / 64], tile_e, tile_m0, n_fill;
   const int tid = threadIdx.x;
   const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  // Rows that no tile computes, each by one workgroup (slots b, b + grid, ...): a padding slot
-  // (negative id) gives zeros, an id >= E NaN.
-  for (int64_t s0 = 0; s0 < TS; s0 += (int64_t)NT * gridDim.x) {
-    if (tid == 0) n_fill = 0;
-    __syncthreads();
-    const int64_t s = s0 + (int64_t)tid * gridDim.x + blockIdx.x;
-    if (s < TS && (unsigned)ids[s] >= (unsigned)E) cnt[atomicAdd(&n_fill, 1)] = (int)s;
-    __syncthreads();
-    for (int k = 0; k < n_fill; k++) {
-      const int at = cnt[k];
-      const float v = ids[at] < 0 ? 0.0f : __builtin_nanf("");
-      for (int64_t n = tid; n < N; n += NT) Y[at * N + n] = v;
-    }
-    __syncthreads();
-  }
   // f(first slot, the ids of four slots; those past the end are -1) for the slots of this wave, a run
-  // of them, 256 at a time in index order, four lots of loads in flight
+  // of them, 256 at a time in index order, four lots of loads in flight; the first four stay in
+  // registers for all three passes over the slots
   const int run = (TS + 256 * (NT / 64) - 1) / (256 * (NT / 64)) * 256, r0 = wave * run;
   const __amdgpu_buffer_rsrc_t rI = __builtin_amdgcn_make_buffer_rsrc((void*)ids, 0, TS * 4, 0x00020000);
+  auto load_ids = [&](int s, mx::u32x4 (&v)[4]) {
+#pragma unroll
+    for (int k = 0; k < 4; k++) v[k] = __builtin_amdgcn_raw_buffer_load_b128(rI, (s + k * 256 + lane * 4) * 4, 0, 0);
+  };
+  mx::u32x4 ids0[4];
+  load_ids(r0, ids0);
   auto for_slots = [&](auto&& f) {
     for (int s = r0; s < r0 + run && s < TS; s += 1024) {
-      mx::u32x4 v[4];
-#pragma unroll
-      for (int k = 0; k < 4; k++) v[k] = __builtin_amdgcn_raw_buffer_load_b128(rI, (s + k * 256 + lane * 4) * 4, 0, 0);
+      mx::u32x4 v[4] = {ids0[0], ids0[1], ids0[2], ids0[3]};
+      if (s > r0) load_ids(s, v);
 #pragma unroll
       for (int k = 0; k < 4; k++) {
         const int at = s + k * 256 + lane * 4;
@@ -336,6 +327,26 @@ __global__ __launch_bounds__(WN* WM* KS * 64) __attribute__((amdgpu_waves_per_eu
       }
     }
   };
+  // Rows that no tile computes, each by one workgroup (slots b, b + grid, ...): a padding slot
+  // (negative id) gives zeros, an id >= E NaN.  Most calls have none.
+  auto outside = [&](int64_t s) { return s < TS && (unsigned)ids[s] >= (unsigned)E; };
+  bool any = false;
+  for (int64_t s = (int64_t)tid * gridDim.x + blockIdx.x; s < TS; s += (int64_t)NT * gridDim.x) any = any || outside(s);
+  if (__syncthreads_or(any)) {
+    for (int64_t s0 = 0; s0 < TS; s0 += (int64_t)NT * gridDim.x) {
+      if (tid == 0) n_fill = 0;
+      __syncthreads();
+      const int64_t s = s0 + (int64_t)tid * gridDim.x + blockIdx.x;
+      if (outside(s)) cnt[atomicAdd(&n_fill, 1)] = (int)s;
+      __syncthreads();
+      for (int k = 0; k < n_fill; k++) {
+        const int at = cnt[k];
+        const float v = ids[at] < 0 ? 0.0f : __builtin_nanf("");
+        for (int64_t n = tid; n < N; n += NT) Y[at * N + n] = v;
+      }
+      __syncthreads();
+    }
+  }
   for (int e = tid; e < E; e += NT) cnt[e] = 0;
   if (tid == 0) tile_e = -1;
   for (int r = tid; r < C::kBM; r += NT) yrow[r] = -1;
@@ -432,19 +443,18 @@ int launch_qmm_mx_as(const uint8_t* wc, const uint8_t* xc, float* Y, int64_t M, 
   return launch_status();
 }
 
-// Workgroups that an indexed product aims at: with fewer (512) the last ones to end leave units idle,
-// with more each counts the slots for less work.
-constexpr int kIdGrid = 2048;
-
 template <int WN, int WM, int TN, int TM, int KS, int OCC>
 int launch_qmm_id_mx_as(const uint8_t* wc, int E, int64_t N, const MxLayout& W, const int32_t* ids, int TS, int top_k, const uint8_t* xc,
-                        const MxLayout& X, int64_t xtr, int64_t xsr, float* Y, hipStream_t s) {
+                        const MxLayout& X, int64_t xtr, int64_t xsr, float* Y, int aim, hipStream_t s) {
   using C = MxTile<WN, WM, TN, TM, KS>;
   const int64_t tn = (N + C::kBN - 1) / C::kBN;
   // row tiles: at most one partial tile per expert that has slots, plus the full ones
   const int64_t tm = (TS < E ? TS : E) + TS / C::kBM > 0 ? (TS < E ? TS : E) + TS / C::kBM : 1;
-  int64_t span = kIdGrid / tm;
+  // about `aim` workgroups, each with the same number of weight tiles as far as that goes
+  int64_t span = (aim + tm / 2) / tm;
   span = span < 1 ? 1 : span < tn ? span : tn;
+  const int64_t each = (tn + span - 1) / span;
+  span = (tn + each - 1) / each;
   if (tm * span > kMaxGrid || tn > INT32_MAX) return BQM_E_SHAPE;
   hipLaunchKernelGGL((k_qmm_id_mxfp4<WN, WM, TN, TM, KS, OCC>), dim3((unsigned)(tm * span)), dim3(C::kThreads), 0, s, wc, W.scales_off, xc,
                      X.scales_off, ids, Y, E, N, (int)W.ks, (int)W.kg, TS, top_k, xtr, xsr, X.rt, (int)tn, (int)span);
@@ -501,17 +511,22 @@ int launch_qmm_id_mxfp4(const void* w, int E, int64_t N, int64_t K, const int32_
   const uint8_t* wc = static_cast<const uint8_t*>(w);
   const uint8_t* xc = static_cast<const uint8_t*>(x);
   if (!mx_fits(W) || X.scales_off >= ((int64_t)1 << 31)) return BQM_E_SHAPE;
-  // The tile by the slots of an expert if all were used alike: a taller tile streams the weights of
-  // busy experts less often, a lower one spends less on empty rows.  Measured (us; 128 experts, top-8,
-  // a skewed router, 1536 x 4096 per expert): 512 tokens 89 with 128 x 128 (128 x 64: 94, 128 x 32:
-  // 105), 128 tokens 40 with 128 x 64 (43, 46), 16 tokens 22.8 with 128 x 32 (128 x 64: 23.6, 64 x 16
-  // in four shares of K: 25.5), one token 7.7 with 64 x 16 (128 x 32: 10.1).
+  // The tile by the slots of an expert if all were used alike: a wide and tall tile reads gathered rows
+  // and the weights of busy experts less often, a smaller one spends less on empty rows.  `aim`: with
+  // more workgroups each counts the slots for less work, with fewer the last ones to end leave units
+  // idle.  Measured (us; 128 experts, top-8, a skewed router, 1536 x 4096 per expert): 4096 tokens 361
+  // with 256 x 128 (256 x 64: 379, 128 x 128: 450), 512: 87 with 256 x 64 (128 x 128: 89, 256 x 128:
+  // 96), 128: 41 with 128 x 64 (256 x 64: 47), 16: 23 with 128 x 32 (128 x 64: 24, 64 x 16 in four
+  // shares of K: 25), one 7.7 with 64 x 16 (128 x 32: 10.1); aiming at 1536 instead of 1024, 2048
+  // tokens take 218 and not 190, 128 tokens at 2048 take 46 and not 41, 16 tokens at 1024 26 and not 23.
   const int TS = T * top_k, used = TS < E ? TS : E > 0 ? E : 1;
-#define BQM_MX_ID(...) launch_qmm_id_mx_as<__VA_ARGS__>(wc, E, N, W, ids, TS, top_k, xc, X, x_tok_rows, x_slot_rows, Y, s)
-  if ((int64_t)used * ((N + 63) / 64) <= 768 && TS <= 2 * used) return BQM_MX_ID(1, 1, 4, 1, 4, 2);
-  if (TS >= 24 * used) return BQM_MX_ID(2, 2, 4, 4, 1, 2);
-  if (TS >= 6 * used) return BQM_MX_ID(2, 2, 4, 2, 1, 3);
-  return BQM_MX_ID(2, 1, 4, 2, 1, 2);
+#define BQM_MX_ID(aim, ...) \
+  launch_qmm_id_mx_as<__VA_ARGS__>(wc, E, N, W, ids, TS, top_k, xc, X, x_tok_rows, x_slot_rows, Y, aim, s)
+  if ((int64_t)used * ((N + 63) / 64) <= 768 && TS <= 2 * used) return BQM_MX_ID(2048, 1, 1, 4, 1, 4, 2);
+  if (TS >= 48 * used) return BQM_MX_ID(1024, 4, 2, 4, 4, 1, 2);
+  if (TS >= 12 * used) return BQM_MX_ID(1536, 4, 1, 4, 4, 1, 2);
+  if (TS >= 6 * used) return BQM_MX_ID(1024, 2, 2, 4, 2, 1, 3);
+  return BQM_MX_ID(2048, 2, 1, 4, 2, 1, 2);
 #undef BQM_MX_ID
 }
 

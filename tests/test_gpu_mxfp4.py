@@ -279,7 +279,8 @@ def test_qmm_extreme_scales_and_empty():
 
 @pytest.mark.parametrize("per_slot", [False, True])
 @pytest.mark.parametrize("T,E,top_k,N,K", [(1, 8, 2, 33, 128), (1, 128, 8, 64, 544), (3, 5, 3, 200, 96), (17, 6, 2, 48, 1024),
-                                           (40, 3, 2, 130, 288), (150, 4, 3, 100, 160), (600, 7, 1, 40, 64), (9, 300, 8, 17, 32)])
+                                           (40, 3, 2, 130, 288), (150, 4, 3, 100, 160), (600, 7, 1, 40, 64), (9, 300, 8, 17, 32),
+                                           (20, 4, 2, 70, 160), (256, 128, 8, 3300, 32), (1600, 128, 8, 1100, 32)])
 def test_qmm_id(T, E, top_k, N, K, per_slot):
     say("qmm_id_mxfp4", T, E, top_k, N, K, per_slot)
     w = blocks(E * N, K, ("mxi", E, N, K))
