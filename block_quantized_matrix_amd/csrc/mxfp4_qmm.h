@@ -437,7 +437,6 @@ int launch_qmm_mx_as(const uint8_t* wc, const uint8_t* xc, float* Y, int64_t M, 
                      hipStream_t s) {
   using C = MxTile<WN, WM, TN, TM, KS>;
   const int64_t tm = (M + C::kBM - 1) / C::kBM, tn = (N + C::kBN - 1) / C::kBN;
-  if (tm * tn > kMaxGrid) return BQM_E_SHAPE;
   hipLaunchKernelGGL((k_qmm_mxfp4<WN, WM, TN, TM, KS, OCC>), dim3((unsigned)(tm * tn)), dim3(C::kThreads), 0, s, wc, W.scales_off, xc,
                      X.scales_off, Y, M, N, (int)W.ks, (int)W.kg, (int)tm, (int)tn);
   return launch_status();
@@ -474,7 +473,8 @@ static bool mx_fits(const MxLayout& L) { return L.ks <= BQM_MXFP4_MAX_K / mx::kS
 // (128 x 64: 39, 256 x 256: 37), 64: 12.1 with 128 x 64 in two shares of K (in one: 14.8), 16: 10.5
 // with 128 x 32 in four (64 x 16 in eight: 14.8); 8192^3: 265 with 256 x 256 (128 x 128: 304).  N x K
 // = 5120 x 17408: 512 tokens 38.5 with 128 x 128 in two shares (in one: 48.6), 64: 15.1 with
-// 64 x 32 in eight, one: 11.3 with 32 x 16 in sixteen.
+// 64 x 32 in eight, one: 11.3 with 32 x 16 in sixteen.  256 x 128 tiles gained nowhere: 4096 tokens 228
+// with waves of 64 x 64, 243 with waves of 128 x 64, whose registers spill.
 int launch_qmm_mxfp4(const void* w, const void* x, float* Y, int64_t M, int64_t N, int64_t K, hipStream_t s) {
   const MxLayout W = mx_layout(N, K), X = mx_layout(M, K);
   if (!mx_fits(W)) return BQM_E_SHAPE;
@@ -495,6 +495,7 @@ int launch_qmm_mxfp4(const void* w, const void* x, float* Y, int64_t M, int64_t 
   double least = 0;
   for (const Choice& c : all) {
     const int64_t wgs = ((M + c.bm - 1) / c.bm) * ((N + c.bn - 1) / c.bn), load = (wgs + 255) / 256;
+    if (wgs > kMaxGrid) continue;
     const int64_t steps = (W.kg + c.shares - 1) / c.shares * 4;
     const double t = (double)(steps < W.ks ? steps : W.ks) * (load == 1 ? c.one : load * c.full) + 2.0 + load;
     if (!best || t < least) {
@@ -502,7 +503,7 @@ int launch_qmm_mxfp4(const void* w, const void* x, float* Y, int64_t M, int64_t 
       least = t;
     }
   }
-  return best->launch(wc, xc, Y, M, N, W, X, s);
+  return best ? best->launch(wc, xc, Y, M, N, W, X, s) : BQM_E_SHAPE;
 }
 
 int launch_qmm_id_mxfp4(const void* w, int E, int64_t N, int64_t K, const int32_t* ids, int T, int top_k, const void* x,

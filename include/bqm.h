@@ -308,7 +308,8 @@ int bqm_dequantize_mxfp4(const void* packed, int y_type, void* Y, int64_t y_stri
 /* Decode GEMV and small-batch GEMV with MXFP4 weights, qmv_q4_0's counterpart:
  *     Y[m][n] = sum_k dequant(W)[n][k] * X[m][k],   0 <= m < M <= 8, 0 <= n < N,   X and Y fp32.
  * Same tolerance and status codes; each input counts exactly down to a resolution of 2^-133, and
- * weights beyond fp32's range (scales above 2^125) as infinite.  K <= BQM_MXFP4_MAX_K. */
+ * weights beyond fp32's range (scales above 2^125) as infinite.  K above BQM_MXFP4_MAX_K, N above 2^29:
+ * BQM_E_SHAPE. */
 #define BQM_MXFP4_MAX_K (1 << 23)
 int qmv_mxfp4(const void* w_packed, const float* X, float* Y, int M, int64_t N, int64_t K, hipStream_t stream);
 
@@ -317,7 +318,8 @@ int qmv_mxfp4(const void* w_packed, const float* X, float* Y, int M, int64_t N, 
  * w_packed: packed N x K.  x_packed: packed M x K, from bqm_quantize_mxfp4.  Products of codes are
  * exact and block scales are powers of two; the sums are fp32.  Any M from one token on.  A block
  * of either operand with scale byte 255 makes the outputs of its row NaN.  K above
- * BQM_MXFP4_MAX_K: BQM_E_SHAPE (qmm_id_mxfp4 too, and where the activations' codes reach 2 GiB). */
+ * BQM_MXFP4_MAX_K: BQM_E_SHAPE (qmm_id_mxfp4 too, and where the activations' codes reach 2 GiB), and so
+ * are outputs that take 2^22 tiles of 256 x 256 or more. */
 int qmm_mxfp4(const void* w_packed, const void* x_packed, float* Y, int64_t M, int64_t N, int64_t K, hipStream_t stream);
 
 /* Expert-indexed qmm_mxfp4, qmm_id's counterpart:

@@ -328,6 +328,43 @@ def test_qmm_id_long_prompt():
         close(host(Y), np.where(pad, 0, np.take_along_axis(every, at, 1)), np.where(pad, 0, np.take_along_axis(size, at, 1)), K, "long")
 
 
+def test_offsets_past_32_bits():
+    """Codes of more than 4 GiB and rows of more than 2^32 values: every call, checked at rows on both sides."""
+    N, K, E = 1050003, 8192, 3
+    say("large offsets", N, K)
+    g = torch.Generator(DEV).manual_seed(11)
+    b = torch.randint(0, 256, (N, K // 32, 17), dtype=torch.uint8, device=DEV, generator=g)
+    b[..., 0] = torch.randint(118, 133, (N, K // 32), dtype=torch.uint8, device=DEV, generator=g)
+    w = room(N, K)
+    bqm.bqm_repack("mxfp4", b, w, N, K)
+    assert torch.equal(unpacked(w, N, K), b)
+    rows = torch.tensor([0, 15, 16, N // 3, N // 3 - 1, N // 2, 2 * (N // 3), (1 << 20) - 1, 1 << 20, N - 17, N - 1], device=DEV)
+    raw = host(b[rows])
+    del b
+    W = _mxref.dequantize(raw)
+    for M in (1, 8):
+        X, Y = gen.normal((M, K), ("mxo", M)), torch.empty((M, N), device=DEV)
+        bqm.qmv_mxfp4(w, X.to(DEV), Y, M, N, K)
+        close(host(Y[:, rows]), *_mxref.product(W, X.numpy().astype(np.float64)), K, "qmv")
+    for M in (3, 300):
+        x, Y = blocks(M, K, ("mxo-x", M)), torch.empty((M, N), device=DEV)
+        bqm.qmm_mxfp4(w, packed(x), Y, M, N, K)
+        close(host(Y[:, rows]), *_mxref.product(W, _mxref.dequantize(x)), K, "qmm")
+        ids = torch.arange(M, dtype=torch.int32, device=DEV).remainder(E)[:, None].contiguous()
+        Y = torch.empty((M, N // E), device=DEV)
+        bqm.qmm_id_mxfp4(w, E, N // E, K, ids, M, 1, packed(x), M, 1, 0, Y)
+        want, S = _mxref.product(W, _mxref.dequantize(x))
+        for k, row in enumerate(rows.tolist()):
+            e, n = divmod(row, N // E)
+            mine = slice(e, M, E)
+            close(host(Y[mine, n]), want[mine, k], S[mine, k], K, "qmm_id")
+    y = torch.empty((N, K), dtype=torch.bfloat16, device=DEV)
+    bqm.bqm_dequantize_mxfp4(w, y, K, N, K)
+    assert np.array_equal(host(y[rows].float()).astype(np.float64), W)  # codes times powers of two are exact in bf16
+    bqm.bqm_quantize_mxfp4(y, K, w, N, K)
+    assert np.array_equal(host(unpacked(w, N, K)[rows]), _mxref.quantize(W))
+
+
 # ---- together, and in graphs ----
 
 def layer(T, E, top_k, H, F, key):

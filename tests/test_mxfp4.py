@@ -78,6 +78,10 @@ def test_product_refusals():
         for at in range(3):
             for bad, status in ((None, NULL), (ODD, ALIGN)):
                 assert f(*[bad if i == at else GOOD for i in range(3)]) == status
+    assert L.qmv_mxfp4(GOOD, GOOD, GOOD, 1, (1 << 29) + 1, 64, None) == SHAPE
+    assert L.qmv_mxfp4(GOOD, GOOD, GOOD, 1, 64, (1 << 23) + 32, None) == SHAPE
+    assert L.qmm_mxfp4(GOOD, GOOD, GOOD, 1, 64, (1 << 23) + 32, None) == SHAPE
+    assert L.qmm_mxfp4(GOOD, GOOD, GOOD, 1 << 30, 64, 64, None) == SHAPE  # 2^22 tiles
     assert L.qmm_mxfp4(GOOD, GOOD, GOOD, -1, 64, 64, None) == SHAPE
     assert L.qmm_mxfp4(GOOD, GOOD, GOOD, 1, 64, 33, None) == SHAPE
     assert L.qmv_mxfp4(None, None, None, 0, 64, 64, None) == 0
