@@ -185,12 +185,16 @@ def _type(t):
 
 def _call_on(t, stream, name, *args):
     """The call on t's device, where that is another than the current one too."""
-    d = t.device.index if isinstance(t, torch.Tensor) else None
-    if d is None or d == torch.cuda.current_device():
+    d = t.get_device() if isinstance(t, torch.Tensor) else -1
+    if d < 0:
         _call(name, *args, _stream(stream))
+        return
+    s = torch._C._cuda_getCurrentRawStream(d) if stream is None else stream.cuda_stream
+    if d == torch._C._cuda_getDevice():
+        _call(name, *args, s)
     else:
         with torch.cuda.device(d):
-            _call(name, *args, _stream(stream))
+            _call(name, *args, s)
 
 
 def bqm_quantize_mxfp4(X, x_stride: int, packed, rows: int, K: int, stream=None):
