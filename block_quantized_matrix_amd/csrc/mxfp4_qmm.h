@@ -283,15 +283,14 @@ __global__ __launch_bounds__(WN* WM* KS * 64) __attribute__((amdgpu_waves_per_eu
 
 // ---- expert-indexed product ----
 // Every workgroup counts the slots per expert, cuts each expert's slots (in index order) into row
-// tiles of kBM and numbers them, experts ascending; workgroup b takes row tile b / span, and of the
-// weight tiles those with tile % span == b % span, one after another: the slots are counted once for
-// all of them.  Workgroups past the last row tile only take part in filling the rows that no tile
-// computes.
+// tiles of kBM and numbers them, experts ascending; item i is row tile i / span with those weight tiles
+// that have tile % span == i % span, one after another: the slots are counted once for all of them.
+// Workgroups past the last item only take part in filling the rows that no tile computes.
 template <int WN, int WM, int TN, int TM, int KS, int OCC>
 __global__ __launch_bounds__(WN* WM* KS * 64) __attribute__((amdgpu_waves_per_eu(OCC, OCC))) void k_qmm_id_mxfp4(
     const uint8_t* __restrict__ w, int64_t w_scales, const uint8_t* __restrict__ x, int64_t x_scales, const int32_t* __restrict__ ids,
     float* __restrict__ Y, int E, int64_t N, int ks, int kg, int TS, int top_k, int64_t xtr, int64_t xsr, int64_t x_tiles, int tiles_n,
-    int span) {
+    int span, int deal) {
   using C = MxTile<WN, WM, TN, TM, KS>;
   constexpr int NT = C::kThreads;
   __shared__ __attribute__((aligned(16))) uint8_t lds0[KS * C::kStage];
@@ -348,7 +347,6 @@ __global__ __launch_bounds__(WN* WM* KS * 64) __attribute__((amdgpu_waves_per_eu
     }
   }
   for (int e = tid; e < E; e += NT) cnt[e] = 0;
-  if (tid == 0) tile_e = -1;
   for (int r = tid; r < C::kBM; r += NT) yrow[r] = -1;
   __syncthreads();
   for_slots([&](int, const int(&id)[4]) {
@@ -359,7 +357,7 @@ __global__ __launch_bounds__(WN* WM* KS * 64) __attribute__((amdgpu_waves_per_eu
   __syncthreads();
   // the expert and the first of its slots that this workgroup's row tile holds: thread t looks at a
   // run of experts, after a sum of the tile counts over the threads before it
-  const int tm = blockIdx.x / span, per = (E + NT - 1) / NT;
+  const int per = (E + NT - 1) / NT;
   const int e0 = tid * per < E ? tid * per : E, e1 = e0 + per < E ? e0 + per : E;
   int tiles = 0;
   for (int e = e0; e < e1; e++) tiles += (cnt[e] + C::kBM - 1) / C::kBM;
@@ -372,7 +370,18 @@ __global__ __launch_bounds__(WN* WM* KS * 64) __attribute__((amdgpu_waves_per_eu
   if (lane == 63) wsum[wave] = before;
   __syncthreads();
   before -= tiles;
-  for (int k = 0; k < wave; k++) before += wsum[k];
+  int all_tiles = 0;
+#pragma unroll
+  for (int k = 0; k < NT / 64; k++) {
+    before += k < wave ? wsum[k] : 0;
+    all_tiles += wsum[k];
+  }
+  // item of this workgroup: in order, or dealt so that an XCD (workgroups go round them) has a run of them
+  const int items = __builtin_amdgcn_readfirstlane(all_tiles) * span, mask = (1 << deal) - 1;
+  const int run_at = blockIdx.x & mask, more = items & mask, nth = blockIdx.x >> deal;
+  if (nth >= (items >> deal) + (run_at < more)) return;  // none left, the whole workgroup
+  const int item = run_at * (items >> deal) + (run_at < more ? run_at : more) + nth;
+  const int tm = item / span;
   if (tm >= before && tm < before + tiles)
     for (int e = e0; e < e1; e++) {
       const int k = (cnt[e] + C::kBM - 1) / C::kBM;
@@ -385,7 +394,6 @@ __global__ __launch_bounds__(WN* WM* KS * 64) __attribute__((amdgpu_waves_per_eu
     }
   __syncthreads();
   const int e = __builtin_amdgcn_readfirstlane(tile_e), m0 = __builtin_amdgcn_readfirstlane(tile_m0);
-  if (e < 0) return;  // past the last row tile, the whole workgroup
   const int rows = cnt[e] - m0 < C::kBM ? cnt[e] - m0 : C::kBM;
   // its slots: those of rank m0 and up among the expert's, the waves before this one counted first
   int found = 0;
@@ -421,7 +429,7 @@ __global__ __launch_bounds__(WN* WM* KS * 64) __attribute__((amdgpu_waves_per_eu
   __syncthreads();
   const MxOperand xo = mx_operand(x, x_scales, 0, x_tiles, ks, kg);
   const int64_t all = ((int64_t)E * N + 15) >> 4;
-  for (int tn = blockIdx.x % span; tn < tiles_n; tn += span) {
+  for (int tn = item - tm * span; tn < tiles_n; tn += span) {
     const int64_t n0 = (int64_t)tn * C::kBN, at = (int64_t)e * N + n0;
     const int nr = (int)(N - n0 < C::kBN ? N - n0 : C::kBN), off = (int)(at & 15);
     mx_core<WN, WM, TN, TM, KS>(
@@ -444,7 +452,7 @@ int launch_qmm_mx_as(const uint8_t* wc, const uint8_t* xc, float* Y, int64_t M, 
 
 template <int WN, int WM, int TN, int TM, int KS, int OCC>
 int launch_qmm_id_mx_as(const uint8_t* wc, int E, int64_t N, const MxLayout& W, const int32_t* ids, int TS, int top_k, const uint8_t* xc,
-                        const MxLayout& X, int64_t xtr, int64_t xsr, float* Y, int aim, hipStream_t s) {
+                        const MxLayout& X, int64_t xtr, int64_t xsr, float* Y, int aim, int deal, hipStream_t s) {
   using C = MxTile<WN, WM, TN, TM, KS>;
   const int64_t tn = (N + C::kBN - 1) / C::kBN;
   // row tiles: at most one partial tile per expert that has slots, plus the full ones
@@ -456,7 +464,7 @@ int launch_qmm_id_mx_as(const uint8_t* wc, int E, int64_t N, const MxLayout& W, 
   span = (tn + each - 1) / each;
   if (tm * span > kMaxGrid || tn > INT32_MAX) return BQM_E_SHAPE;
   hipLaunchKernelGGL((k_qmm_id_mxfp4<WN, WM, TN, TM, KS, OCC>), dim3((unsigned)(tm * span)), dim3(C::kThreads), 0, s, wc, W.scales_off, xc,
-                     X.scales_off, ids, Y, E, N, (int)W.ks, (int)W.kg, TS, top_k, xtr, xsr, X.rt, (int)tn, (int)span);
+                     X.scales_off, ids, Y, E, N, (int)W.ks, (int)W.kg, TS, top_k, xtr, xsr, X.rt, (int)tn, (int)span, deal);
   return launch_status();
 }
 
@@ -515,14 +523,17 @@ int launch_qmm_id_mxfp4(const void* w, int E, int64_t N, int64_t K, const int32_
   // The tile by the slots of an expert if all were used alike: a wide and tall tile reads gathered rows
   // and the weights of busy experts less often, a smaller one spends less on empty rows.  `aim`: with
   // more workgroups each counts the slots for less work, with fewer the last ones to end leave units
-  // idle.  Measured (us; 128 experts, top-8, a skewed router, 1536 x 4096 per expert): 4096 tokens 361
+  // idle.  Measured in order (us; 128 experts, top-8, a skewed router, 1536 x 4096 each): 4096 tokens 361
   // with 256 x 128 (256 x 64: 379, 128 x 128: 450), 512: 87 with 256 x 64 (128 x 128: 89, 256 x 128:
   // 96), 128: 41 with 128 x 64 (256 x 64: 47), 16: 23 with 128 x 32 (128 x 64: 24, 64 x 16 in four
   // shares of K: 25), one 7.7 with 64 x 16 (128 x 32: 10.1); aiming at 1536 instead of 1024, 2048
   // tokens take 218 and not 190, 128 tokens at 2048 take 46 and not 41, 16 tokens at 1024 26 and not 23.
-  const int TS = T * top_k, used = TS < E ? TS : E > 0 ? E : 1;
+  // Items are dealt to the XCDs in eight runs where experts have few row tiles (16 tokens 21.4, in order
+  // 23.1; 64: 34 and 36.7; 256: 68 and 71), and taken in order where several row tiles share the weights in
+  // the last cache (512 tokens 88, dealt 95; 4096: 371 and 403).
+  const int TS = T * top_k, used = TS < E ? TS : E > 0 ? E : 1, deal = TS >= 24 * used ? 0 : 3;
 #define BQM_MX_ID(aim, ...) \
-  launch_qmm_id_mx_as<__VA_ARGS__>(wc, E, N, W, ids, TS, top_k, xc, X, x_tok_rows, x_slot_rows, Y, aim, s)
+  launch_qmm_id_mx_as<__VA_ARGS__>(wc, E, N, W, ids, TS, top_k, xc, X, x_tok_rows, x_slot_rows, Y, aim, deal, s)
   if ((int64_t)used * ((N + 63) / 64) <= 768 && TS <= 2 * used) return BQM_MX_ID(2048, 1, 1, 4, 1, 4, 2);
   if (TS >= 48 * used) return BQM_MX_ID(1024, 4, 2, 4, 4, 1, 2);
   if (TS >= 12 * used) return BQM_MX_ID(1536, 4, 1, 4, 4, 1, 2);
