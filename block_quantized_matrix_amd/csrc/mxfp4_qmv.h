@@ -76,11 +76,10 @@ __global__ __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(OCC, OCC
   const int64_t r0 = (int64_t)blockIdx.x * a.halves * 8, t0 = r0 >> 4;
   const int64_t r1 = r0 + a.halves * 8 < a.N ? r0 + a.halves * 8 : a.N;
   const int64_t cb = (a.tiles - t0) * a.ks * mx::kOperand, sb = (a.tiles - t0) * a.kg * mx::kScaleTile, most = 0x7FFFFFFF;
-  const __amdgpu_buffer_rsrc_t rc =
-      __builtin_amdgcn_make_buffer_rsrc((void*)(a.w + t0 * a.ks * mx::kOperand), 0, (int)(cb < most ? cb : most), 0x00020000);
-  const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc((void*)(a.w + a.scales_off + t0 * a.kg * mx::kScaleTile), 0,
-                                                                      (int)(sb < most ? sb : most), 0x00020000);
-  const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc((void*)a.x, 0, (int)(a.M * a.K * 4), 0x00020000);
+  // a step past the last finds nothing (and moves nothing): its descriptors are empty
+  auto within = [&](const void* p, int64_t bytes, int s) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, s < a.ks ? (int)(bytes < most ? bytes : most) : 0, 0x00020000);
+  };
   uint32_t oc[T], os[T];
 #pragma unroll
   for (int t = 0; t < T; t++) {
@@ -98,28 +97,31 @@ __global__ __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(OCC, OCC
     const int item = r * 64 + lane, m = item >> 4;
     ox[r] = m < a.M ? (uint32_t)(m * (int)a.K + (item >> 2 & 3) * 32 + (item & 3) * 4) * 4 : kMxOob;
   }
-  // a step past the last reads zeros
   auto load_x = [&](int d, int s) {
-    const bool any = s < a.ks;
+    const __amdgpu_buffer_rsrc_t rx = within(a.x, a.M * a.K * 4, s);
 #pragma unroll
     for (int r = 0; r < R; r++) {
-      const uint32_t at = 4 * s + (lane >> 2 & 3) < nb ? ox[r] : kMxOob;  // and so does a block past the row's end
-      xa[d][r] = __builtin_amdgcn_raw_buffer_load_b128(rx, at, any ? s * 512 : 0, 0);
-      xb[d][r] = __builtin_amdgcn_raw_buffer_load_b128(rx, at + 64, any ? s * 512 : 0, 0);
+      const uint32_t at = 4 * s + (lane >> 2 & 3) < nb ? ox[r] : kMxOob;  // a block past the row's end is not read
+      xa[d][r] = __builtin_amdgcn_raw_buffer_load_b128(rx, at, s * 512, 0);
+      xb[d][r] = __builtin_amdgcn_raw_buffer_load_b128(rx, at + 64, s * 512, 0);
     }
   };
   auto load_w = [&](int d, int t, int s) {
-    const bool any = s < a.ks;
-    code[d][t] = __builtin_amdgcn_raw_buffer_load_b128(rc, any ? oc[t] : kMxOob, any ? s * mx::kOperand : 0, 0);
-    scale[d][t] = __builtin_amdgcn_raw_buffer_load_b8(rs, any ? os[t] : kMxOob, any ? (s >> 2) * mx::kScaleTile + (s & 3) : 0, 0);
+    code[d][t] = __builtin_amdgcn_raw_buffer_load_b128(within(a.w + t0 * a.ks * mx::kOperand, cb, s), oc[t], s * mx::kOperand, 0);
+    scale[d][t] = __builtin_amdgcn_raw_buffer_load_b8(within(a.w + a.scales_off + t0 * a.kg * mx::kScaleTile, sb, s), os[t],
+                                                      (s >> 2) * mx::kScaleTile + (s & 3), 0);
   };
   uint8_t* mine = lds + wave * kWave;
   mx::f32x4 acc[T][CT] = {};
 #pragma unroll
   for (int d = 0; d < D; d++) {
     load_x(d, wave + d * W);
+    __builtin_amdgcn_sched_barrier(0);  // in the loop's order, by which it waits
 #pragma unroll
-    for (int t = 0; t < T; t++) load_w(d, t, wave + d * W);
+    for (int t = 0; t < T; t++) {
+      load_w(d, t, wave + d * W);
+      __builtin_amdgcn_sched_barrier(0);
+    }
   }
   for (int s0 = wave; s0 < a.ks; s0 += D * W) {
 #pragma unroll
@@ -140,6 +142,7 @@ __global__ __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(OCC, OCC
 #pragma unroll
           for (int p = 0; p < 3; p++) *reinterpret_cast<mx::u32x4*>(mine + at * lot + (3 * m + p) * 16) = part[p];
       }
+      __builtin_amdgcn_sched_barrier(0);
       load_x(d, s + D * W);  // loads are issued in the order of their use, each as soon as its registers are free
       mx::wave_turn();
       mma::bf16x8 b[4][CT];
@@ -163,6 +166,7 @@ __global__ __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(OCC, OCC
 #pragma unroll
           for (int c = 0; c < CT; c++) acc[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, b[k][c], acc[t][c], 0, 0, 0);
         }
+        __builtin_amdgcn_sched_barrier(0);
         load_w(d, t, s + D * W);
       }
       mx::wave_turn();  // the next step's inputs go where these were read
@@ -208,10 +212,12 @@ int launch_mxv(const MxvArgs& a, int64_t grid, hipStream_t s) {
 
 // One workgroup per compute unit, or as many rounds of them as nine tiles each make, so that all end
 // together: sixteen waves where a unit has up to two tiles of rows, eight with registers for more
-// tiles above.  Measured (us): 4096 x 4096, one input, 4.8 (eight waves 5.7; two workgroups a
-// unit 7.5); 5120 x 17408 at batch 8 20.2 (eight waves 22.0, two a unit 31.9); 34816 x 5120
-// with eight waves 20.1, 4.7 TB/s (sixteen and two rounds 27.1), at batch 8 24.3 (38.8).  Loads
-// two steps ahead instead of one gained nothing from three tiles on (34816 x 5120: 22.8).
+// tiles above.  Measured (us): 4096 x 4096, one input, 4.5 (eight waves 5.7; two workgroups a
+// unit 7.5; 4.8 where the loads past the end were branches); 5120 x 17408 at batch 8 20.7 (eight waves
+// 22.0, two a unit 31.9); 34816 x 5120 with eight waves 20.0, 4.7 TB/s (sixteen and two rounds 27.1), at
+// batch 8 23.6 (38.8).  Loads two steps ahead instead of one gained nothing from two tiles on (5120 x 17408
+// at batch 8: 23.4), nor did runs of four rows, which give every unit as many (7168 x 5120: 7.2, 5.7
+// with eight).
 int launch_qmv_mxfp4(const void* w, const float* X, float* Y, int M, int64_t N, int64_t K, hipStream_t s) {
   const MxLayout L = mx_layout(N, K);
   if (K > BQM_MXFP4_MAX_K || N > ((int64_t)1 << 29)) return BQM_E_SHAPE;  // the grid stays below kMaxGrid
