@@ -227,7 +227,8 @@ static int launch_dequantize_as(const void* packed, void* Y, int64_t stride, int
   const uint8_t* codes = static_cast<const uint8_t*>(packed);
   const int64_t units = L.rt * L.ks;
   hipLaunchKernelGGL(k_dequantize_mxfp4<TYPE>, unit_grid(units), dim3(kPackThreads), 0, s, codes, codes + L.scales_off,
-                     static_cast<typename Elem<TYPE>::T*>(Y), stride, (int)(stride * (int)sizeof(typename Elem<TYPE>::T) % 16 == 0), rows, K / kQK, L.ks, L.kg, units);
+                     static_cast<typename Elem<TYPE>::T*>(Y), stride, (int)(stride * (int)sizeof(typename Elem<TYPE>::T) % 16 == 0),
+                     rows, K / kQK, L.ks, L.kg, units);
   return launch_status();
 }
 

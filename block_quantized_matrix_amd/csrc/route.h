@@ -298,8 +298,7 @@ __global__ __launch_bounds__(WAVES * 64) void k_route(RouteArgs a) {
     place[k] = k * G + lane;
   }
   bool again = true, weighed = false;
-  // (one token's latency is less without it)
-  if constexpr (V * G <= 256 && (G == 16 || (!BIAS && sizeof(Elem) == 2))) {
+  if constexpr (V * G <= 256) {
     // The fp32 pass.  A sigmoid is within kOff of the real one: the product x log2 e and v_exp_f32 move
     // e^-x by 1.25 |x| + 2 steps of 2^-24 of it, which s (1 - s) |x| <= 0.23 makes 0.8 steps of 1; the
     // sum, v_rcp_f32 add 3: below 2^-22.  A softmax's terms and its sum of 256 (16 in turn, then a
@@ -516,7 +515,8 @@ int launch_route_as(int score, const RouteArgs& a, hipStream_t s) {
 }
 
 // Sixteen lanes a token from 1024 tokens on (16384 x 128, top-8: 4.6 us), where that fills the chip's
-// units; below, 64 lanes a token end sooner (512 x 256 with a bias in groups: 9 us).
+// units; below, 64 lanes a token end sooner (one token of 256 experts with a bias 4.4 us, in groups 6.3; 512 in
+// groups 6.9; with 64 bits throughout 5.7, 7.9 and 8.7).
 template <int TYPE>
 int launch_route_type(int score, const RouteArgs& a, hipStream_t s) {
   if (a.E <= 256 && a.T >= 1024)
