@@ -63,6 +63,20 @@ def test_groups(E, n_group, topk_group, top_k, score):
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,n_group,topk_group,top_k", [(256, 8, 3, 8), (60, 3, 1, 6)])
+@pytest.mark.parametrize("T", [5, 1101])
+def test_group_sums_beyond_fp32(T, E, n_group, topk_group, top_k, score):
+    """Biases whose sums pass the range of fp32, or lie on its last step, keep the order that 64 bits give them."""
+    say("route group sums", T, E, n_group, topk_group, top_k, score)
+    l = gen.normal((T, E), ("route-o", T, E), device=DEV)
+    g = torch.arange(n_group, dtype=torch.float64)
+    for base, step in ((2.0e38, 2.0e35), (1.0, 2.0 ** -22)):
+        bias = torch.zeros(n_group, E // n_group, dtype=torch.float64)
+        bias[:, 0], bias[:, 3] = base + step * g, base
+        check(l, bias.reshape(-1).float().to(DEV), score, n_group, topk_group, 2, top_k, True, 1.0)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_ties_go_to_the_lower_index(score):
     say("route ties", score)
     l = torch.from_numpy(np.random.default_rng(2).integers(-2, 3, (60, 96)).astype(np.float32)).to(DEV)
