@@ -166,7 +166,7 @@ __global__ __launch_bounds__(WAVES * 64) void k_route(RouteArgs a) {
     for (int k = 0; k < kKept; k++)
       if (s == k * G + lane) kept[k] = id;
   };
-  // The groups that stay open, one bit each, from the lanes' values of type T; near: whether two
+  // The groups that stay open, one bit each, from the lanes' values of type T; near: set where two
   // groups are within `margin` (negative: never).
   const int size = a.size;
   const bool whole = size % V == 0 && V > 1;  // a lane's experts are of one group
@@ -252,7 +252,7 @@ __global__ __launch_bounds__(WAVES * 64) void k_route(RouteArgs a) {
     const bool in = before < a.topk_group;
     const float low = reduce<G>(in ? w : __builtin_inff(), [](float p, float q) { return __builtin_fminf(p, q); });
     const float high = reduce<G>(in ? -__builtin_inff() : w, [](float p, float q) { return __builtin_fmaxf(p, q); });
-    near = margin >= 0 && high > -__builtin_inff() && !(low - high > margin);
+    near = near || (margin >= 0 && high > -__builtin_inff() && !(low - high > margin));
     return in;
   };
   // f(v, whether the group of expert e0 + v is open)
@@ -333,7 +333,9 @@ __global__ __launch_bounds__(WAVES * 64) void k_route(RouteArgs a) {
       for (int v = 0; v < V; v++) most = BIAS ? __builtin_fmaxf(most, __builtin_fabsf(bias[v])) : 0.0f;
       if (BIAS) most = reduce<G>(most, [](float p, float q) { return __builtin_fmaxf(p, q); });
       const float margin = scored ? 4.0f * (kOff + 0x1p-23f * (1 + most)) : -1.0f;
-      bool near = false;
+      // Sums of such biases can leave the range of fp32, and an infinite sum says nothing of its place:
+      // below, it equals that of a group without an expert.
+      bool near = sums && most > 0x1p126f;  // 2 (1 + 2^126) is far inside
       auto value = [&](int v) { return !BIAS && sums && val[v] > -__builtin_inff() ? score[v] : val[v]; };
       uint64_t open = 0;
       bool own = true;
