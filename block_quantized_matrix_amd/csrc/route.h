@@ -78,7 +78,7 @@ __device__ __forceinline__ void count_down(F&& f) {
 
 // e^x by x = n ln 2 + r, |r| <= ln 2 / 2, and the Taylor series of e^r to r^13 / 13! (the next term
 // is below 2^-57): within two steps of 64 bits, in half the operations of the library's, which the
-// scores of 256 experts make felt.  x in [-1000, 709].
+// scores of 256 experts make felt.  x in [-1000, 1024 ln 2].
 __device__ __forceinline__ double exp64(double x) {
   const double n = __builtin_rint(x * 0x1.71547652b82fep0);
   double r = fma(n, -0x1.62e42fefa39efp-1, x);
@@ -91,17 +91,18 @@ __device__ __forceinline__ double exp64(double x) {
   for (int k = 0; k < 13; k++) p = fma(p, r, c[k]);
   return __builtin_ldexp(p, (int)n);
 }
-// 1 / x for x in [1, 2^1023]: the hardware's estimate and two Newton steps.
+// 1 / x for x in [1, 2^1024): the hardware's estimate and two Newton steps.
 __device__ __forceinline__ double rcp64(double x) {
   double y = __builtin_amdgcn_rcp(x);
   y = fma(fma(-x, y, 1.0), y, y);
   return fma(fma(-x, y, 1.0), y, y);
 }
-// 1 / (1 + e^-x); where e^-x passes the range of 64 bits, 0.
+// 1 / (1 + e^-x); where e^-x passes the range of 64 bits (x below -1024 ln 2), 0.
 __device__ __forceinline__ double sigmoid64(float x) {
+  constexpr double kEnd = 0x1.62e42fefa39efp+9;
   const double l = x;
-  const double s = rcp64(1.0 + exp64(fmin(fmax(-l, -709.0), 709.0)));
-  return l < -709.0 ? 0.0 : s;
+  const double s = rcp64(1.0 + exp64(fmin(fmax(-l, -kEnd), kEnd)));
+  return l < -kEnd ? 0.0 : s;
 }
 
 // BIAS: the order is that of scores with their bias, 64 bits; without it that of the logits as they

@@ -1,5 +1,5 @@
 """The router at the ends of its numbers' ranges, against the plain 64-bit form: sums of two biases below fp32's range,
-and groups of more than 256 experts."""
+sigmoid scores at the end of 64 bits, and groups of more than 256 experts."""
 import numpy as np
 import pytest
 import torch
@@ -63,6 +63,22 @@ def test_masked_groups_by_hand():
         bias[16:48] = torch.finfo(torch.float32).min
         ids, w = route(l, bias, "sigmoid", 4, 2, 2, 18, True, 1.0)
         assert (ids == np.r_[48:64, 16:18]).all() and (w == np.float32(1 / 18)).all()
+
+
+@pytest.mark.parametrize("T", [4, 1030])
+@pytest.mark.parametrize("E", [40, 200, 300])
+def test_sigmoid_at_the_end_of_64_bits(E, T):
+    """Scores down to the reciprocal of the largest 64-bit number, 709.78 below zero, where they are 0 from there on."""
+    say("route sigmoid end", E, T)
+    l = torch.linspace(-709.9, -708.2, E, device=DEV).repeat(T, 1)
+    l[1::2] = l[1::2].flip(1)
+    zero, bias = torch.zeros(E, device=DEV), torch.zeros(E, device=DEV)
+    l[2, 6:], bias[:3] = -800.0, -1.0  # scores of 0 beside six small ones
+    l[2, :6] = torch.linspace(-709.78, -708.2, 6)
+    for b in (None, zero, bias):
+        for renorm in (True, False):
+            check(l, b, "sigmoid", 1, 1, 1, 8, renorm, 1.0)
+    check(l, zero, "sigmoid", 4, 2, 2, 8, True, 1.0)
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
