@@ -57,6 +57,36 @@ __device__ __forceinline__ void mxv_split(const float (&a)[4], const float (&b)[
     mxv_parts<false>(a, b, part);
 }
 
+// A step of a tile where scale bytes may be above 252, whose largest weights bf16 does not hold: infinite,
+// they would come out as NaN beside those parts of an input that are 0.  A row with such a byte (among the
+// step's four, which lanes i, i + 16, ... hold for row i) takes all its weights at a quarter, exact in bf16
+// down to the lowest scale, and its sum times four.
+template <int CT>
+__device__ __forceinline__ void mxv_far_step(const mx::u32x4& code, uint32_t scale, const mma::bf16x8 (&b)[4][CT], int q,
+                                             mx::f32x4 (&acc)[CT]) {
+  uint64_t rows = __ballot(scale > 252 && scale < 255);
+  rows |= rows >> 32;
+  rows |= rows >> 16;
+  const uint32_t far = (uint32_t)rows & 0xFFFF;
+  const float f = mx::scale_of(scale) * (far >> (threadIdx.x & 15) & 1 ? 0.25f : 1.0f);
+  mx::f32x4 sum[CT] = {};
+#pragma unroll
+  for (int k = 0; k < 4; k++) {
+    const mx::f32x2 v[4] = {mx::pair_of<0>(code[k], 1.0f), mx::pair_of<1>(code[k], 1.0f), mx::pair_of<2>(code[k], 1.0f),
+                            mx::pair_of<3>(code[k], 1.0f)};
+    mx::u32x4 w;
+#pragma unroll
+    for (int j = 0; j < 4; j++) w[j] = __builtin_amdgcn_perm(__float_as_uint(v[j].y * f), __float_as_uint(v[j].x * f), 0x07060302u);
+#pragma unroll
+    for (int c = 0; c < CT; c++)
+      sum[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(mma::bf16x8, w), b[k][c], sum[c], 0, 0, 0);
+  }
+#pragma unroll
+  for (int c = 0; c < CT; c++)
+#pragma unroll
+    for (int r = 0; r < 4; r++) acc[c][r] += sum[c][r] * (far >> (4 * q + r) & 1 ? 4.0f : 1.0f);
+}
+
 // A workgroup takes `halves` runs of eight rows (a run is a whole 128-byte line of a step's codes),
 // at most T tiles of 16, its W waves the steps of 128 k in turn: wave w the steps w, w + W, ...  A
 // wave splits the inputs of its step once (R items of eight a lane), turns them to the
@@ -123,36 +153,42 @@ __global__ __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(OCC, OCC
       __builtin_amdgcn_sched_barrier(0);
     }
   }
+  auto split = [&](int d) {  // the inputs of a step, as parts, to this wave's LDS
+#pragma unroll
+    for (int r = 0; r < R; r++) {
+      const int item = r * 64 + lane, m = item >> 4, at = (item & 3) * 4 + (item >> 2 & 3);
+      float fa[4], fb[4];
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        fa[j] = __uint_as_float(xa[d][r][j]);
+        fb[j] = __uint_as_float(xb[d][r][j]);
+      }
+      mx::u32x4 part[3];
+      mxv_split(fa, fb, part);
+      if (m < a.M)
+#pragma unroll
+        for (int p = 0; p < 3; p++) *reinterpret_cast<mx::u32x4*>(mine + at * lot + (3 * m + p) * 16) = part[p];
+    }
+  };
+  auto columns = [&](mma::bf16x8 (&b)[4][CT]) {  // and from there
+#pragma unroll
+    for (int t = 0; t < 4; t++)
+#pragma unroll
+      for (int c = 0; c < CT; c++) {
+        const int col = c * 16 + i < cols ? c * 16 + i : cols - 1;  // columns not in use repeat one that is
+        b[t][c] = *reinterpret_cast<const mma::bf16x8*>(mine + (t * 4 + q) * lot + col * 16);
+      }
+  };
   for (int s0 = wave; s0 < a.ks; s0 += D * W) {
 #pragma unroll
     for (int d = 0; d < D; d++) {
       const int s = s0 + d * W;
-#pragma unroll
-      for (int r = 0; r < R; r++) {
-        const int item = r * 64 + lane, m = item >> 4, at = (item & 3) * 4 + (item >> 2 & 3);
-        float fa[4], fb[4];
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-          fa[j] = __uint_as_float(xa[d][r][j]);
-          fb[j] = __uint_as_float(xb[d][r][j]);
-        }
-        mx::u32x4 part[3];
-        mxv_split(fa, fb, part);
-        if (m < a.M)
-#pragma unroll
-          for (int p = 0; p < 3; p++) *reinterpret_cast<mx::u32x4*>(mine + at * lot + (3 * m + p) * 16) = part[p];
-      }
+      split(d);
       __builtin_amdgcn_sched_barrier(0);
       load_x(d, s + D * W);  // loads are issued in the order of their use, each as soon as its registers are free
       mx::wave_turn();
       mma::bf16x8 b[4][CT];
-#pragma unroll
-      for (int t = 0; t < 4; t++)
-#pragma unroll
-        for (int c = 0; c < CT; c++) {
-          const int col = c * 16 + i < cols ? c * 16 + i : cols - 1;  // columns not in use repeat one that is
-          b[t][c] = *reinterpret_cast<const mma::bf16x8*>(mine + (t * 4 + q) * lot + col * 16);
-        }
+      columns(b);
 #pragma unroll
       for (int t = 0; t < T; t++) {
         const float f = __uint_as_float(scale[d][t] << 23);  // the conversion goes by the exponent field alone
@@ -170,6 +206,35 @@ __global__ __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(OCC, OCC
         load_w(d, t, s + D * W);
       }
       mx::wave_turn();  // the next step's inputs go where these were read
+    }
+  }
+  // Sums that are not finite (from such scales, from a NaN scale, from the inputs) are made again with
+  // mxv_far_step.  Looking at the sums costs 0.03 to 0.1 us (4096 x 4096, one input: 4.49 -> 4.52, 34816 x
+  // 5120: 16.2 -> 16.3); looking at each scale in the loop cost 0.5 us there.
+  float probe[4] = {};
+#pragma unroll
+  for (int t = 0; t < T; t++)
+#pragma unroll
+    for (int c = 0; c < CT; c++)
+#pragma unroll
+      for (int r = 0; r < 4; r++) probe[r] += acc[t][c][r];
+  if (__builtin_expect(__any(!__builtin_isfinite((probe[0] + probe[1]) + (probe[2] + probe[3]))), 0)) {  // this wave's steps again
+#pragma unroll
+    for (int t = 0; t < T; t++)
+#pragma unroll
+      for (int c = 0; c < CT; c++) acc[t][c] = mx::f32x4{};
+    for (int s = wave; s < a.ks; s += W) {
+      load_x(0, s);
+      split(0);
+      mx::wave_turn();
+      mma::bf16x8 b[4][CT];
+      columns(b);
+#pragma unroll
+      for (int t = 0; t < T; t++) {
+        load_w(0, t, s);
+        mxv_far_step<CT>(code[0][t], scale[0][t], b, q, acc[t]);
+      }
+      mx::wave_turn();
     }
   }
 #pragma unroll

@@ -307,9 +307,9 @@ int bqm_dequantize_mxfp4(const void* packed, int y_type, void* Y, int64_t y_stri
 
 /* Decode GEMV and small-batch GEMV with MXFP4 weights, qmv_q4_0's counterpart:
  *     Y[m][n] = sum_k dequant(W)[n][k] * X[m][k],   0 <= m < M <= 8, 0 <= n < N,   X and Y fp32.
- * Same tolerance and status codes; each input counts exactly down to a resolution of 2^-133, and
- * weights beyond fp32's range (scales above 2^125) as infinite.  K above BQM_MXFP4_MAX_K, N above 2^29:
- * BQM_E_SHAPE. */
+ * Same tolerance and status codes; each input counts exactly down to a resolution of 2^-133, and each
+ * weight as it is, also those beyond fp32's largest number (scales above 2^125).  K above BQM_MXFP4_MAX_K,
+ * N above 2^29: BQM_E_SHAPE. */
 #define BQM_MXFP4_MAX_K (1 << 23)
 int qmv_mxfp4(const void* w_packed, const float* X, float* Y, int M, int64_t N, int64_t K, hipStream_t stream);
 
