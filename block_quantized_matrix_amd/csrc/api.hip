@@ -365,7 +365,7 @@ const char* bqm_strerror(int status) {
     case BQM_E_NULL: return "a required pointer is NULL";
     case BQM_E_SHAPE: return "invalid size (negative, K not a multiple of 32, or over a limit)";
     case BQM_E_ALIGN: return "a pointer or stride is not suitably aligned (16 bytes)";
-    case BQM_E_UNSUPPORTED: return "unknown block format";
+    case BQM_E_UNSUPPORTED: return "unknown block format, element type or score, or a format that the call does not take";
     case BQM_E_LAUNCH: return "the HIP runtime refused a kernel launch";
     default: return "unknown status";
   }

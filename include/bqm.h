@@ -62,7 +62,7 @@ typedef enum {
   BQM_E_NULL = 1,        /* a required pointer is NULL                          */
   BQM_E_SHAPE = 2,       /* negative size, K % 32 != 0, or a size over a limit  */
   BQM_E_ALIGN = 3,       /* a pointer is not 16-byte aligned                    */
-  BQM_E_UNSUPPORTED = 4, /* unknown format code                                 */
+  BQM_E_UNSUPPORTED = 4, /* an unknown or refused format, type or score         */
   BQM_E_LAUNCH = 5       /* the HIP runtime refused a launch                    */
 } bqm_status;
 

@@ -156,3 +156,9 @@ def test_route_reference_by_hand():
     # two groups of three, sums of the best two scores: group 0 holds 3 and 3
     ids, _ = _mxref.route(l[:1], None, "sigmoid", 2, 1, 2, 4, False, 1.0)
     assert ids.tolist() == [[1, 2, 0, -1]]
+
+
+def test_text_of_unsupported():
+    """The status that an unknown format, element type or score gets says so."""
+    for word in ("format", "type", "score"):
+        assert word in bqm.strerror(UNSUPPORTED)
