@@ -484,35 +484,63 @@ static bool mx_fits(const MxLayout& L) { return L.ks <= BQM_MXFP4_MAX_K / mx::kS
 // 290).  N x K = 5120 x 17408: 512 tokens 38.5 with 128 x 128 in two shares (in one: 48.6), 64: 15.1
 // with 64 x 32 in eight, one: 11.3 with 32 x 16 in sixteen.  256 x 128 tiles gained nowhere: 4096 tokens 228
 // with waves of 64 x 64, 243 with waves of 128 x 64, whose registers spill.
-int launch_qmm_mxfp4(const void* w, const void* x, float* Y, int64_t M, int64_t N, int64_t K, hipStream_t s) {
-  const MxLayout W = mx_layout(N, K), X = mx_layout(M, K);
-  if (!mx_fits(W)) return BQM_E_SHAPE;
-  const uint8_t* wc = static_cast<const uint8_t*>(w);
-  const uint8_t* xc = static_cast<const uint8_t*>(x);
-  struct Choice {
-    int bn, bm, shares;
-    float one, full;
-    int (*launch)(const uint8_t*, const uint8_t*, float*, int64_t, int64_t, const MxLayout&, const MxLayout&, hipStream_t);
-  };
-  static constexpr Choice all[] = {
-      {256, 256, 1, 0.84f, 0.97f, launch_qmm_mx_as<2, 4, 8, 4, 1, 2>}, {128, 128, 1, 0.35f, 0.27f, launch_qmm_mx_as<2, 2, 4, 4, 1, 3>},
-      {128, 128, 2, 0.54f, 0.85f, launch_qmm_mx_as<2, 2, 4, 4, 2, 2>}, {128, 64, 2, 0.40f, 0.44f, launch_qmm_mx_as<2, 2, 4, 2, 2, 4>},
-      {128, 32, 4, 0.55f, 0.83f, launch_qmm_mx_as<2, 1, 4, 2, 4, 2>},  {64, 64, 4, 0.50f, 0.77f, launch_qmm_mx_as<1, 1, 4, 4, 4, 1>},
-      {64, 32, 8, 0.78f, 1.30f, launch_qmm_mx_as<1, 1, 4, 2, 8, 2>},   {64, 16, 8, 0.73f, 1.06f, launch_qmm_mx_as<1, 1, 4, 1, 8, 2>},
-      {32, 16, 16, 1.30f, 1.80f, launch_qmm_mx_as<1, 1, 2, 1, 16, 4>}};
-  const Choice* best = nullptr;
+struct MxChoice {
+  int bn, bm, shares;
+  float one, full;
+  int (*launch)(const uint8_t*, const uint8_t*, float*, int64_t, int64_t, const MxLayout&, const MxLayout&, hipStream_t);
+};
+static constexpr MxChoice kMxChoices[] = {
+    {256, 256, 1, 0.84f, 0.97f, launch_qmm_mx_as<2, 4, 8, 4, 1, 2>}, {128, 128, 1, 0.35f, 0.27f, launch_qmm_mx_as<2, 2, 4, 4, 1, 3>},
+    {128, 128, 2, 0.54f, 0.85f, launch_qmm_mx_as<2, 2, 4, 4, 2, 2>}, {128, 64, 2, 0.40f, 0.44f, launch_qmm_mx_as<2, 2, 4, 2, 2, 4>},
+    {128, 32, 4, 0.55f, 0.83f, launch_qmm_mx_as<2, 1, 4, 2, 4, 2>},  {64, 64, 4, 0.50f, 0.77f, launch_qmm_mx_as<1, 1, 4, 4, 4, 1>},
+    {64, 32, 8, 0.78f, 1.30f, launch_qmm_mx_as<1, 1, 4, 2, 8, 2>},   {64, 16, 8, 0.73f, 1.06f, launch_qmm_mx_as<1, 1, 4, 1, 8, 2>},
+    {32, 16, 16, 1.30f, 1.80f, launch_qmm_mx_as<1, 1, 2, 1, 16, 4>}};
+
+// The index of the tile, -1 where none has room for the outputs.  (The tests ask too: they have to run
+// every tile.)
+extern "C" int bqm_internal_qmm_mxfp4_choice(int64_t M, int64_t N, int64_t K) {
+  const MxLayout W = mx_layout(N, K);
+  int best = -1;
   double least = 0;
-  for (const Choice& c : all) {
+  for (const MxChoice& c : kMxChoices) {
     const int64_t wgs = ((M + c.bm - 1) / c.bm) * ((N + c.bn - 1) / c.bn), load = (wgs + 255) / 256;
     if (wgs > kMaxGrid) continue;
     const int64_t steps = (W.kg + c.shares - 1) / c.shares * 4;
     const double t = (double)(steps < W.ks ? steps : W.ks) * (load == 1 ? c.one : load * c.full) + 2.0 + load;
-    if (!best || t < least) {
-      best = &c;
+    if (best < 0 || t < least) {
+      best = (int)(&c - kMxChoices);
       least = t;
     }
   }
-  return best ? best->launch(wc, xc, Y, M, N, W, X, s) : BQM_E_SHAPE;
+  return best;
+}
+
+int launch_qmm_mxfp4(const void* w, const void* x, float* Y, int64_t M, int64_t N, int64_t K, hipStream_t s) {
+  const MxLayout W = mx_layout(N, K), X = mx_layout(M, K);
+  if (!mx_fits(W)) return BQM_E_SHAPE;
+  const int c = bqm_internal_qmm_mxfp4_choice(M, N, K);
+  if (c < 0) return BQM_E_SHAPE;
+  return kMxChoices[c].launch(static_cast<const uint8_t*>(w), static_cast<const uint8_t*>(x), Y, M, N, W, X, s);
+}
+
+// Experts that have slots, at most.
+static int mx_used(int E, int TS) { return TS < E ? TS : E > 0 ? E : 1; }
+
+// The tile by the slots of an expert if all were used alike: a wide and tall tile reads gathered rows
+// and the weights of busy experts less often, a smaller one spends less on empty rows.  `aim`: with
+// more workgroups each counts the slots for less work, with fewer the last ones to end leave units
+// idle.  Measured in order (us; 128 experts, top-8, a skewed router, 1536 x 4096 each): 4096 tokens 361
+// with 256 x 128 (256 x 64: 379, 128 x 128: 450), 512: 87 with 256 x 64 (128 x 128: 89, 256 x 128:
+// 96), 128: 41 with 128 x 64 (256 x 64: 47), 16: 23 with 128 x 32 (128 x 64: 24, 64 x 16 in four
+// shares of K: 25), one 7.7 with 64 x 16 (128 x 32: 10.1); aiming at 1536 instead of 1024, 2048
+// tokens take 218 and not 190, 128 tokens at 2048 take 46 and not 41, 16 tokens at 1024 26 and not 23.
+// Items are dealt to the XCDs in eight runs where experts have few row tiles (16 tokens 21.4, in order
+// 23.1; 64: 34 and 36.7; 256: 68 and 71), and taken in order where several row tiles share the weights in
+// the last cache (512 tokens 88, dealt 95; 4096: 371 and 403).
+extern "C" int bqm_internal_qmm_id_mxfp4_choice(int E, int64_t N, int TS) {
+  const int used = mx_used(E, TS);
+  if ((int64_t)used * ((N + 63) / 64) <= 768 && TS <= 2 * used) return 0;
+  return TS >= 48 * used ? 1 : TS >= 12 * used ? 2 : TS >= 6 * used ? 3 : 4;
 }
 
 int launch_qmm_id_mxfp4(const void* w, int E, int64_t N, int64_t K, const int32_t* ids, int T, int top_k, const void* x,
@@ -521,25 +549,16 @@ int launch_qmm_id_mxfp4(const void* w, int E, int64_t N, int64_t K, const int32_
   const uint8_t* wc = static_cast<const uint8_t*>(w);
   const uint8_t* xc = static_cast<const uint8_t*>(x);
   if (!mx_fits(W) || X.scales_off >= ((int64_t)1 << 31)) return BQM_E_SHAPE;
-  // The tile by the slots of an expert if all were used alike: a wide and tall tile reads gathered rows
-  // and the weights of busy experts less often, a smaller one spends less on empty rows.  `aim`: with
-  // more workgroups each counts the slots for less work, with fewer the last ones to end leave units
-  // idle.  Measured in order (us; 128 experts, top-8, a skewed router, 1536 x 4096 each): 4096 tokens 361
-  // with 256 x 128 (256 x 64: 379, 128 x 128: 450), 512: 87 with 256 x 64 (128 x 128: 89, 256 x 128:
-  // 96), 128: 41 with 128 x 64 (256 x 64: 47), 16: 23 with 128 x 32 (128 x 64: 24, 64 x 16 in four
-  // shares of K: 25), one 7.7 with 64 x 16 (128 x 32: 10.1); aiming at 1536 instead of 1024, 2048
-  // tokens take 218 and not 190, 128 tokens at 2048 take 46 and not 41, 16 tokens at 1024 26 and not 23.
-  // Items are dealt to the XCDs in eight runs where experts have few row tiles (16 tokens 21.4, in order
-  // 23.1; 64: 34 and 36.7; 256: 68 and 71), and taken in order where several row tiles share the weights in
-  // the last cache (512 tokens 88, dealt 95; 4096: 371 and 403).
-  const int TS = T * top_k, used = TS < E ? TS : E > 0 ? E : 1, deal = TS >= 24 * used ? 0 : 3;
+  const int TS = T * top_k, used = mx_used(E, TS), deal = TS >= 24 * used ? 0 : 3;
 #define BQM_MX_ID(aim, ...) \
   launch_qmm_id_mx_as<__VA_ARGS__>(wc, E, N, W, ids, TS, top_k, xc, X, x_tok_rows, x_slot_rows, Y, aim, deal, s)
-  if ((int64_t)used * ((N + 63) / 64) <= 768 && TS <= 2 * used) return BQM_MX_ID(2048, 1, 1, 4, 1, 4, 2);
-  if (TS >= 48 * used) return BQM_MX_ID(1024, 4, 2, 4, 4, 1, 2);
-  if (TS >= 12 * used) return BQM_MX_ID(1536, 4, 1, 4, 4, 1, 2);
-  if (TS >= 6 * used) return BQM_MX_ID(1024, 2, 2, 4, 2, 1, 3);
-  return BQM_MX_ID(2048, 2, 1, 4, 2, 1, 2);
+  switch (bqm_internal_qmm_id_mxfp4_choice(E, N, TS)) {
+    case 0: return BQM_MX_ID(2048, 1, 1, 4, 1, 4, 2);
+    case 1: return BQM_MX_ID(1024, 4, 2, 4, 4, 1, 2);
+    case 2: return BQM_MX_ID(1536, 4, 1, 4, 4, 1, 2);
+    case 3: return BQM_MX_ID(1024, 2, 2, 4, 2, 1, 3);
+    default: return BQM_MX_ID(2048, 2, 1, 4, 2, 1, 2);
+  }
 #undef BQM_MX_ID
 }
 

@@ -283,11 +283,15 @@ int launch_mxv(const MxvArgs& a, int64_t grid, hipStream_t s) {
 // batch 8 23.6 (38.8).  Loads two steps ahead instead of one gained nothing from two tiles on (5120 x 17408
 // at batch 8: 23.4), nor did runs of four rows, which give every unit as many (7168 x 5120: 7.2, 5.7
 // with eight).
+extern "C" int64_t bqm_internal_qmv_mxfp4_runs(int64_t N) {  // of eight rows, of a workgroup
+  const int64_t runs = (N + 7) / 8, rounds = (runs + 256 * 17 - 1) / (256 * 17);
+  return (runs + 256 * rounds - 1) / (256 * rounds);
+}
+
 int launch_qmv_mxfp4(const void* w, const float* X, float* Y, int M, int64_t N, int64_t K, hipStream_t s) {
   const MxLayout L = mx_layout(N, K);
   if (K > BQM_MXFP4_MAX_K || N > ((int64_t)1 << 29)) return BQM_E_SHAPE;  // the grid stays below kMaxGrid
-  const int64_t runs = (N + 7) / 8, rounds = (runs + 256 * 17 - 1) / (256 * 17);
-  const int64_t halves = (runs + 256 * rounds - 1) / (256 * rounds), grid = (runs + halves - 1) / halves;
+  const int64_t halves = bqm_internal_qmv_mxfp4_runs(N), grid = ((N + 7) / 8 + halves - 1) / halves;
   const MxvArgs a{static_cast<const uint8_t*>(w), X, Y, L.scales_off, N, K, L.rt, M, (int)L.ks, (int)L.kg, (int)halves};
   return M <= 4 ? launch_mxv<1, 1>(a, grid, s) : M == 5 ? launch_mxv<2, 1>(a, grid, s) : launch_mxv<2, 2>(a, grid, s);
 }
