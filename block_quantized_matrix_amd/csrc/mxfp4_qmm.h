@@ -474,16 +474,20 @@ int launch_qmm_id_mx_as(const uint8_t* wc, int E, int64_t N, const MxLayout& W, 
 // (and, where rows are gathered, the activations as a whole) stay below 2 GiB.
 static bool mx_fits(const MxLayout& L) { return L.ks <= BQM_MXFP4_MAX_K / mx::kStepK && L.ks * 17 * mx::kOperand < ((int64_t)1 << 31); }
 
-// The dense product's tile, by an estimate of its time from three figures measured for each: `one`,
-// the time of a step where a compute unit holds one workgroup (latency), `full`, its share of a step
-// where it holds several (throughput), and what each workgroup adds (launch, first loads, store).
-// Measured (us, N x K = 17408 x 5120): 4096 tokens 207 with 128 x 128 or 256 x 256, 512: 36.5 with 256 x 256
-// (128 x 128: 35.5, but where the weights come from memory, behind a quantizer, both together 46.9 and 53.2;
-// 600 tokens 46.9 and 52.7), 64: 12.1 with 128 x 64 in two shares of K (in one:
-// 14.8), 16: 10.5 with 128 x 32 in four (64 x 16 in eight: 14.8); 8192^3: 255 with 256 x 256 (128 x 128:
-// 290).  N x K = 5120 x 17408: 512 tokens 38.5 with 128 x 128 in two shares (in one: 48.6), 64: 15.1
-// with 64 x 32 in eight, one: 11.3 with 32 x 16 in sixteen.  256 x 128 tiles gained nowhere: 4096 tokens 228
-// with waves of 64 x 64, 243 with waves of 128 x 64, whose registers spill.
+// The dense product's tile, by an estimate of its time on 256 compute units, from two figures for each:
+// `one`, the time of a step where a unit holds one workgroup (latency), and `full`, its share of a step
+// where it holds several (throughput); 2 us a launch and 1 a round of workgroups are the same for all.
+// Both were measured with weights in the last cache, but for the 0.84 of 256 x 256: measured 0.88, and set
+// lower because that tile reads weights from memory less often, for which the estimate has no term.  It
+// turns products of about 512 tokens its way: with the quantizer and N x K = 17408 x 5120, weights from
+// memory, 512 tokens take 46.9 us (128 x 128: 53.2) and 600 take 46.9 (52.7); with weights in the cache
+// it loses, 36.5 (35.5) and 41.4 (37.3) without the quantizer.  Other N and K at that length were not
+// measured both ways.
+// Measured (us, N x K = 17408 x 5120): 4096 tokens 207 with 128 x 128 or 256 x 256, 64: 12.1 with 128 x 64
+// in two shares of K (in one: 14.8), 16: 10.5 with 128 x 32 in four (64 x 16 in eight: 14.8); 8192^3: 255
+// with 256 x 256 (128 x 128: 290).  N x K = 5120 x 17408: 512 tokens 38.5 with 128 x 128 in two shares (in
+// one: 48.6), 64: 15.1 with 64 x 32 in eight, one: 11.3 with 32 x 16 in sixteen.  256 x 128 tiles gained
+// nowhere: 4096 tokens 228 with waves of 64 x 64, 243 with waves of 128 x 64, whose registers spill.
 struct MxChoice {
   int bn, bm, shares;
   float one, full;
@@ -536,7 +540,9 @@ static int mx_used(int E, int TS) { return TS < E ? TS : E > 0 ? E : 1; }
 // tokens take 218 and not 190, 128 tokens at 2048 take 46 and not 41, 16 tokens at 1024 26 and not 23.
 // Items are dealt to the XCDs in eight runs where experts have few row tiles (16 tokens 21.4, in order
 // 23.1; 64: 34 and 36.7; 256: 68 and 71), and taken in order where several row tiles share the weights in
-// the last cache (512 tokens 88, dealt 95; 4096: 371 and 403).
+// the last cache (512 tokens 88, dealt 95; 4096: 371 and 403).  All of it is from this one layer: with few
+// experts or few outputs the items may be fewer than the units, each over all of K.  A row per slot (4096 x
+// 1536 each): one token 8.3, 16 tokens 23.6, 128: 66, 512: 116, 2048: 331, 4096: 703.
 extern "C" int bqm_internal_qmm_id_mxfp4_choice(int E, int64_t N, int TS) {
   const int used = mx_used(E, TS);
   if ((int64_t)used * ((N + 63) / 64) <= 768 && TS <= 2 * used) return 0;

@@ -277,10 +277,10 @@ int launch_mxv(const MxvArgs& a, int64_t grid, hipStream_t s) {
 
 // One workgroup per compute unit, or as many rounds of them as nine tiles each make, so that all end
 // together: sixteen waves where a unit has up to two tiles of rows, eight with registers for more
-// tiles above.  Measured (us): 4096 x 4096, one input, 4.5 (eight waves 5.7; two workgroups a
-// unit 7.5; 4.8 where the loads past the end were branches); 5120 x 17408 at batch 8 20.7 (eight waves
-// 22.0, two a unit 31.9); 34816 x 5120 with eight waves 20.0, 4.7 TB/s (sixteen and two rounds 27.1), at
-// batch 8 23.6 (38.8).  Loads two steps ahead instead of one gained nothing from two tiles on (5120 x 17408
+// tiles above.  Measured (us, weights from memory but for the first): 4096 x 4096, one input, 4.5 (eight
+// waves 5.7; two workgroups a unit 7.5; 4.8 where the loads past the end were branches; from memory 5.4);
+// 5120 x 17408 at batch 8 20.9 (eight waves 22.0, two a unit 31.9); 34816 x 5120 with eight waves 19.3,
+// 4.9 TB/s (sixteen and two rounds 27.1), at batch 8 22.9 (38.8).  Loads two steps ahead instead of one gained nothing from two tiles on (5120 x 17408
 // at batch 8: 23.4), nor did runs of four rows, which give every unit as many (7168 x 5120: 7.2, 5.7
 // with eight).
 extern "C" int64_t bqm_internal_qmv_mxfp4_runs(int64_t N) {  // of eight rows, of a workgroup

@@ -18,8 +18,9 @@
 // the differences in 32 bits that wrap round, 24 instructions for a lane's sixteen keys where
 // striking out the key taken had 40; groups are compared by DPP rotations; a bias comes by way of
 // LDS (from memory, a lane's sixteen apart, 14.7 us).  Measured (16384 tokens, 256 experts, top-8):
-// without a bias 5.9 us, sigmoid with a bias 9.3, in groups 12 to 14 (the rare wave that selects again
-// ends last); with 64 bits throughout 10, 22 and 25.  Sorting each lane's keys and merging the
+// without a bias 5.9 us, sigmoid with a bias 9.3, in groups 11 to 14 (the rare wave that selects again
+// ends last; 20 where a bias is -infinity, whose size counts in the groups' margin); with 64 bits
+// throughout 10, 22 and 25.  Sorting each lane's keys and merging the
 // lanes' sorted lists instead of rounds: 7.8, 14.7, 18.3, where these rounds took 6.4, 15.0, 20.4.
 #pragma once
 
@@ -519,7 +520,9 @@ int launch_route_as(int score, const RouteArgs& a, hipStream_t s) {
 
 // Sixteen lanes a token from 1024 tokens on (16384 x 128, top-8: 4.6 us), where that fills the chip's
 // units; below, 64 lanes a token end sooner (one token of 256 experts with a bias 4.4 us, in groups 6.3; 512 in
-// groups 6.9; with 64 bits throughout 5.7, 7.9 and 8.7).
+// groups 6.9; with 64 bits throughout 5.7, 7.9 and 8.7).  Above 256 experts the keys have no room for the
+// expert: 64 bits throughout, and the same instance for 257 as for 1024 (16384 x 384 or x 512: 34 us without
+// a bias, 67 with one, 76 in groups; x 1024 with a bias 70).
 template <int TYPE>
 int launch_route_type(int score, const RouteArgs& a, hipStream_t s) {
   if (a.E <= 256 && a.T >= 1024)
