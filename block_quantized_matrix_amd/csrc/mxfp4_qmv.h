@@ -209,8 +209,9 @@ __global__ __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(OCC, OCC
     }
   }
   // Sums that are not finite (from such scales, from a NaN scale, from the inputs) are made again with
-  // mxv_far_step.  Looking at the sums costs 0.03 to 0.1 us (4096 x 4096, one input: 4.49 -> 4.52, 34816 x
-  // 5120: 16.2 -> 16.3); looking at each scale in the loop cost 0.5 us there.
+  // mxv_far_step.  Looking at the sums costs 0.03 to 0.3 us (4096 x 4096, one input: 4.49 -> 4.52, 34816 x
+  // 5120: 16.2 -> 16.3, 5120 x 17408 with five: 14.1 -> 14.4); looking at each scale in the loop: 16.7 for
+  // the second.
   float probe[4] = {};
 #pragma unroll
   for (int t = 0; t < T; t++)
