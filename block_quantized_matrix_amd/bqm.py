@@ -23,6 +23,7 @@ MXFP4 = 39
 FMT = {"q4_0": Q4_0, "q8_0": Q8_0, "mxfp4": MXFP4}
 TYPE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 30}  # bqm_type
 SCORE = {"softmax": 0, "sigmoid": 1}
+ACT = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 QMV_MAX_M = 8
 QMV_ID_MAX_T = 64
 QMM_ID_MAX_T = 16384
@@ -72,8 +73,11 @@ def lib():
         L.qmm_mxfp4.argtypes = [P, P, P, I64, I64, I64, P]
         L.qmm_id_mxfp4.argtypes = [P, I, I64, I64, P, I, I, P, I64, I64, I64, P, P]
         L.bqm_route.argtypes = [I, I, P, I64, P, I, I, I, I, I, I, I, ctypes.c_float, P, P, P]
+        L.bqm_embed.argtypes = [I, P, I64, I64, P, I64, ctypes.c_float, I, P, I64, P]
+        L.bqm_linear.argtypes = [I, P, I, P, I64, P, I, P, I64, P, I64, I, P, I64, I64, I64, I64, P]
+        L.bqm_linear_grouped.argtypes = [I, P, I, P, I, P, I64, P, I, P, I64, P, I64, I, P, I64, I64, I64, I64, P]
         for f in ("bqm_quantize_mxfp4", "bqm_dequantize_mxfp4", "qmv_mxfp4", "qmm_mxfp4", "qmm_id_mxfp4",
-                  "bqm_route"):
+                  "bqm_route", "bqm_embed", "bqm_linear", "bqm_linear_grouped"):
             getattr(L, f).restype = I
         for f in ("bqm_chain_prepare", "qmv_chain", "bqm_chain_status"):
             getattr(L, f).restype = I
@@ -226,6 +230,36 @@ def bqm_route(score, logits, l_stride: int, bias, T: int, E: int, n_group: int, 
     """score: "softmax" or "sigmoid"; logits of fp32, fp16 or bf16, rows l_stride elements apart; bias: fp32 or None."""
     _call_on(ids, stream, "bqm_route", SCORE.get(score, -1), _type(logits), _ptr(logits), l_stride, _ptr(bias), T, E, n_group,
           topk_group, group_top, top_k, int(renorm), scale, _ptr(ids), _ptr(weights))
+
+
+def bqm_embed(fmt, w_packed, rows: int, K: int, ids, T: int, scale: float, Y, y_stride: int, stream=None):
+    """Rows ids (int32) of a packed table, times scale -> rows of Y's dtype, y_stride elements apart."""
+    y_type = _type(Y) if ids is None or ids.dtype == torch.int32 else -1  # the library refuses an unknown type
+    _call_on(Y, stream, "bqm_embed", _fmt(fmt), _ptr(w_packed), rows, K, _ptr(ids), T, scale, y_type, _ptr(Y), y_stride)
+
+
+def _epilogue_type(Y, bias, mul, residual, offsets=None):
+    """Y's type, unless an operand beside it is of another than it has to be."""
+    fits = ((bias is None or bias.dtype == torch.float32) and (offsets is None or offsets.dtype == torch.int32)
+            and (mul is None or mul.dtype == Y.dtype) and (residual is None or residual.dtype == Y.dtype))
+    return _type(Y) if fits else -1
+
+
+def bqm_linear(fmt, w_packed, X, x_stride: int, Y, y_stride: int, M: int, N: int, K: int, bias=None, act="none",
+               mul=None, mul_stride: int = 0, residual=None, res_stride: int = 0, stream=None):
+    """Y = act(X W^T + bias) * mul + residual; X of fp32, fp16 or bf16, bias fp32, mul and residual of Y's dtype."""
+    _call_on(Y, stream, "bqm_linear", _fmt(fmt), _ptr(w_packed), _type(X), _ptr(X), x_stride, _ptr(bias), ACT.get(act, -1),
+             _ptr(mul), mul_stride, _ptr(residual), res_stride, _epilogue_type(Y, bias, mul, residual), _ptr(Y), y_stride,
+             M, N, K)
+
+
+def bqm_linear_grouped(fmt, w_packed, E: int, offsets, X, x_stride: int, Y, y_stride: int, R: int, N: int, K: int,
+                       bias=None, act="none", mul=None, mul_stride: int = 0, residual=None, res_stride: int = 0,
+                       stream=None):
+    """bqm_linear where rows offsets[e] .. offsets[e + 1] - 1 (int32 [E + 1]) take matrix e and bias e."""
+    _call_on(Y, stream, "bqm_linear_grouped", _fmt(fmt), _ptr(w_packed), E, _ptr(offsets), _type(X), _ptr(X), x_stride,
+             _ptr(bias), ACT.get(act, -1), _ptr(mul), mul_stride, _ptr(residual), res_stride,
+             _epilogue_type(Y, bias, mul, residual, offsets), _ptr(Y), y_stride, R, N, K)
 
 
 class Gemv(ctypes.Structure):

@@ -337,6 +337,62 @@ int bqm_route(int score, int l_type, const void* logits, int64_t l_stride, const
                       scale, ids, weights, stream);
 }
 
+static bool any_fmt(int fmt) { return valid_fmt(fmt) || fmt == BQM_MXFP4; }
+
+int bqm_embed(int fmt, const void* w_packed, int64_t rows, int64_t K, const int32_t* ids, int64_t T, float scale,
+              int y_type, void* Y, int64_t y_stride, hipStream_t stream) {
+  if (!any_fmt(fmt) || !valid_type(y_type)) return BQM_E_UNSUPPORTED;
+  if (int st = check_sizes(rows, K)) return st;
+  if (T < 0 || T > kMaxRows || y_stride < K || y_stride > kMaxStride) return BQM_E_SHAPE;
+  if (T == 0 || K == 0) return BQM_OK;
+  if (int st = check_ptr(ids)) return st;
+  if (int st = check_ptr(Y)) return st;
+  if (rows > 0)
+    if (int st = check_ptr(w_packed)) return st;
+  return launch_embed(fmt, w_packed, rows, K, ids, T, scale, y_type, Y, y_stride, stream);
+}
+
+// bqm_linear is the grouped call with one group, without offsets
+static int linear_common(int fmt, const void* w_packed, int E, const int32_t* offsets, int x_type, const void* X,
+                         int64_t x_stride, const float* bias, int act, const void* mul, int64_t mul_stride,
+                         const void* residual, int64_t res_stride, int y_type, void* Y, int64_t y_stride, int64_t R,
+                         int64_t N, int64_t K, bool grouped, hipStream_t stream) {
+  if (!any_fmt(fmt) || !valid_type(x_type) || !valid_type(y_type) || act < BQM_ACT_NONE || act > BQM_ACT_GELU_TANH)
+    return BQM_E_UNSUPPORTED;
+  if (E < 0 || E > BQM_QMV_ID_MAX_E || N < 0 || N > kMaxRows || R < 0 || R > kMaxRows) return BQM_E_SHAPE;
+  if (int st = check_sizes((int64_t)E * N, K)) return st;
+  if (x_stride < K || x_stride > BQM_LINEAR_MAX_K || y_stride < N || y_stride > kMaxStride) return BQM_E_SHAPE;
+  if (mul && (mul_stride < N || mul_stride > kMaxStride)) return BQM_E_SHAPE;
+  if (residual && (res_stride < N || res_stride > kMaxStride)) return BQM_E_SHAPE;
+  if (R == 0 || N == 0 || E == 0) return BQM_OK;
+  if (int st = check_ptr(Y)) return st;
+  if (grouped)
+    if (int st = check_ptr(offsets)) return st;
+  if (K > 0) {
+    if (int st = check_ptr(w_packed)) return st;
+    if (int st = check_ptr(X)) return st;
+    if (x_stride * (x_type == BQM_F32 ? 4 : 2) % 16 != 0) return BQM_E_ALIGN;
+  }
+  if (!aligned16(mul) || !aligned16(residual) || (reinterpret_cast<uintptr_t>(bias) & 3) != 0) return BQM_E_ALIGN;
+  return launch_linear(fmt, w_packed, E, offsets, x_type, X, x_stride, bias, act, mul, mul_stride, residual, res_stride,
+                       y_type, Y, y_stride, R, N, K, stream);
+}
+
+int bqm_linear(int fmt, const void* w_packed, int x_type, const void* X, int64_t x_stride, const float* bias, int act,
+               const void* mul, int64_t mul_stride, const void* residual, int64_t res_stride, int y_type, void* Y,
+               int64_t y_stride, int64_t M, int64_t N, int64_t K, hipStream_t stream) {
+  return linear_common(fmt, w_packed, 1, nullptr, x_type, X, x_stride, bias, act, mul, mul_stride, residual, res_stride,
+                       y_type, Y, y_stride, M, N, K, false, stream);
+}
+
+int bqm_linear_grouped(int fmt, const void* w_packed, int E, const int32_t* offsets, int x_type, const void* X,
+                       int64_t x_stride, const float* bias, int act, const void* mul, int64_t mul_stride,
+                       const void* residual, int64_t res_stride, int y_type, void* Y, int64_t y_stride, int64_t R,
+                       int64_t N, int64_t K, hipStream_t stream) {
+  return linear_common(fmt, w_packed, E, offsets, x_type, X, x_stride, bias, act, mul, mul_stride, residual, res_stride,
+                       y_type, Y, y_stride, R, N, K, true, stream);
+}
+
 size_t bqm_chain_workspace_bytes(int n) { return chain_workspace_bytes(n); }
 
 int bqm_chain_prepare(const bqm_gemv* descs, int n, void* workspace, hipStream_t stream) {
@@ -365,7 +421,7 @@ const char* bqm_strerror(int status) {
     case BQM_E_NULL: return "a required pointer is NULL";
     case BQM_E_SHAPE: return "invalid size (negative, K not a multiple of 32, or over a limit)";
     case BQM_E_ALIGN: return "a pointer or stride is not suitably aligned (16 bytes)";
-    case BQM_E_UNSUPPORTED: return "unknown block format, element type or score, or a format that the call does not take";
+    case BQM_E_UNSUPPORTED: return "unknown block format, element type, score or activation, or a format that the call does not take";
     case BQM_E_LAUNCH: return "the HIP runtime refused a kernel launch";
     default: return "unknown status";
   }

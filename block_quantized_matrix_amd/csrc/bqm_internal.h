@@ -107,6 +107,15 @@ int launch_qmm_id_mxfp4(const void* w, int E, int64_t N, int64_t K, const int32_
 int launch_route(int score, int type, const void* logits, int64_t stride, const float* bias, int64_t T, int E,
                  int n_group, int topk_group, int group_top, int top_k, int renorm, float scale, int32_t* ids,
                  float* weights, hipStream_t s);
+int launch_embed(int fmt, const void* w, int64_t rows, int64_t K, const int32_t* ids, int64_t T, float scale, int y_type,
+                 void* Y, int64_t y_stride, hipStream_t s);
+namespace lin {
+struct Args;  // linear.h
+}
+int launch_linear(int fmt, const void* w, int E, const int32_t* offsets, int x_type, const void* X, int64_t x_stride,
+                  const float* bias, int act, const void* mul, int64_t mul_stride, const void* res, int64_t res_stride,
+                  int y_type, void* Y, int64_t y_stride, int64_t R, int64_t N, int64_t K, hipStream_t s);
+int launch_linear_rows(int fmt, int x_type, const lin::Args& a, int64_t groups, int64_t rows_each, hipStream_t s);
 int launch_fill(float* y, int64_t n, float v, hipStream_t s);
 int cu_count();
 int launch_id_mma(int fmt, const void* w, const void* w_up, int E, int64_t N, int64_t K,

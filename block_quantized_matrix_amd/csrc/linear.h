@@ -1,0 +1,250 @@
+// What the kernels of the linear layer share, gfx950 (device code; included by linear_rows.h and
+// linear_tiles.h):
+//   z[m][n] = bias[n] + sum_b d[n][b] sum_{j<32} c[n][32b+j] x[m][32b+j],   y = act(z) mul + residual
+//
+// Codes meet the rows in the matrix cores, as numbers of the rows' type: a code of any of the formats
+// is exact in bf16 and in fp16, and so are products of two such numbers in fp32.  fp32 rows go as three
+// bf16 parts that add up to them.  A matrix product covers one block of 32 (or half of one, the other
+// half added by the next), so the block's scale, which need not be exact in 16 bits, is applied to its
+// sum by one fp32 FMA.  The only roundings are those of fp32 sums, and the last one to y's type.
+#pragma once
+
+#include "mma_ops.h"
+#include "mxfp4.h"
+
+namespace bqm {
+namespace lin {
+
+struct Args {
+  const uint8_t* w;
+  const uint8_t* x;
+  const float* bias;       // or null
+  const uint8_t* mul;      // or null
+  const uint8_t* res;      // or null
+  uint8_t* y;
+  const int32_t* offsets;  // [E + 1] first rows of the groups, or null: all rows are one group's
+  int64_t N, R, scales_off;
+  int64_t xs, ms, rs, ys;  // row strides: x in bytes, the others in elements
+  int nb, ks, kg, E, act, y_type;
+};
+
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+using mma::bf16x8;
+using mx::f32x4;
+using mx::u32x4;
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+constexpr uint32_t kOob = 0x80000000u;  // an offset past every descriptor: reads 0
+
+__host__ __device__ constexpr int type_size(int type) { return type == BQM_F32 ? 4 : 2; }
+constexpr int parts_of(int type) { return type == BQM_F32 ? 3 : 1; }
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p, int64_t bytes) {
+  const int64_t most = 0x7FFFFFFF;
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)(bytes < 0 ? 0 : bytes < most ? bytes : most), 0x00020000);
+}
+
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+  return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32 | (uint32_t)__builtin_amdgcn_readfirstlane((int)v));
+}
+
+// ---- codes as matrix operands ----
+// 1024 + n is an fp16 number with n in its last bits: bytes are put under 0x64 and what is too much is
+// taken off again, exactly.
+__device__ __forceinline__ uint32_t f16_add(uint32_t v, float by) {
+  const f16x2 r = __builtin_bit_cast(f16x2, v) + f16x2{(_Float16)by, (_Float16)by};
+  return __builtin_bit_cast(uint32_t, r);
+}
+__device__ __forceinline__ uint32_t f16_sixteenth(uint32_t v, float by) {
+  const f16x2 r = __builtin_elementwise_fma(__builtin_bit_cast(f16x2, v), f16x2{(_Float16)0.0625f, (_Float16)0.0625f},
+                                            f16x2{(_Float16)by, (_Float16)by});
+  return __builtin_bit_cast(uint32_t, r);
+}
+// Four codes of a word, one per byte (low nibbles to lo, high ones to hi), as pairs of 16-bit numbers.
+// Q4_0 comes out in units of kUnit.
+template <int FMT, int XT>
+constexpr float kUnit = FMT == BQM_Q4_0 && XT != BQM_F16 ? 0.0625f : 1.0f;
+template <int FMT, int XT>
+__device__ __forceinline__ void nibbles(uint32_t w, uint32_t (&lo)[2], uint32_t (&hi)[2]) {
+  if constexpr (FMT == BQM_MXFP4) {  // the conversion takes the two nibbles of a byte
+    const uint32_t w4 = w >> 4, l = (w & 0x000F000Fu) | (w4 & 0xFFF0FFF0u), h = (w4 & 0x000F000Fu) | ((w >> 8) & 0xFFF0FFF0u);
+    if constexpr (XT == BQM_F16) {
+      lo[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(l, 1.0f, 0));
+      lo[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(l, 1.0f, 2));
+      hi[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(h, 1.0f, 0));
+      hi[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(h, 1.0f, 2));
+    } else {
+      lo[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(l, 1.0f, 0));
+      lo[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(l, 1.0f, 2));
+      hi[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(h, 1.0f, 0));
+      hi[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(h, 1.0f, 2));
+    }
+  } else if constexpr (XT == BQM_F16) {
+    const uint32_t b01 = __builtin_amdgcn_perm(0x64646464u, w, 0x04010400u), b23 = __builtin_amdgcn_perm(0x64646464u, w, 0x04030402u);
+    lo[0] = f16_add(b01 & 0xFF0FFF0Fu, -1032.0f);
+    lo[1] = f16_add(b23 & 0xFF0FFF0Fu, -1032.0f);
+    hi[0] = f16_sixteenth(b01 & 0xFFF0FFF0u, -72.0f);
+    hi[1] = f16_sixteenth(b23 & 0xFFF0FFF0u, -72.0f);
+  } else {
+    const uint32_t l = ((w << 4) ^ 0x80808080u) & 0xF0F0F0F0u, h = (w ^ 0x80808080u) & 0xF0F0F0F0u;
+    lo[0] = mma::bf_pair(mma::sbyte(l, 0), mma::sbyte(l, 1));
+    lo[1] = mma::bf_pair(mma::sbyte(l, 2), mma::sbyte(l, 3));
+    hi[0] = mma::bf_pair(mma::sbyte(h, 0), mma::sbyte(h, 1));
+    hi[1] = mma::bf_pair(mma::sbyte(h, 2), mma::sbyte(h, 3));
+  }
+}
+// Four Q8_0 codes of a word.
+template <int XT>
+__device__ __forceinline__ void bytes(uint32_t w, uint32_t (&v)[2]) {
+  if constexpr (XT == BQM_F16) {
+    const uint32_t u = w ^ 0x80808080u;
+    v[0] = f16_add(__builtin_amdgcn_perm(0x64646464u, u, 0x04010400u), -1152.0f);
+    v[1] = f16_add(__builtin_amdgcn_perm(0x64646464u, u, 0x04030402u), -1152.0f);
+  } else {
+    v[0] = mma::bf_pair(mma::sbyte(w, 0), mma::sbyte(w, 1));
+    v[1] = mma::bf_pair(mma::sbyte(w, 2), mma::sbyte(w, 3));
+  }
+}
+
+// A block's scale from the bits that were loaded for it, in units of the codes.
+template <int FMT, int XT>
+__device__ __forceinline__ float scale_from(uint32_t bits) {
+  if constexpr (FMT == BQM_MXFP4) return mx::scale_of(bits);
+  return (float)__builtin_bit_cast(_Float16, (uint16_t)bits) * kUnit<FMT, XT>;
+}
+
+// ---- rows as matrix operands ----
+// Pairs of numbers as bf16 parts: each the upper half of what the parts before it leave.  ODD: some are
+// infinite or NaN, of which nothing is left (and a NaN whose payload is in the lower half must stay one).
+template <bool ODD>
+__device__ __forceinline__ void parts3(float a, float b, uint32_t& p0, uint32_t& p1, uint32_t& p2) {
+  float f[2] = {a, b};
+  uint32_t u[3][2];
+#pragma unroll
+  for (int p = 0; p < 3; p++)
+#pragma unroll
+    for (int k = 0; k < 2; k++) {
+      u[p][k] = __float_as_uint(f[k]);
+      if (ODD && f[k] != f[k]) u[p][k] |= 0x00400000u;
+      if (p < 2) f[k] -= __uint_as_float(u[p][k] & 0xFFFF0000u);
+      if (ODD && !__builtin_isfinite(f[k])) f[k] = 0;
+    }
+  p0 = __builtin_amdgcn_perm(u[0][1], u[0][0], 0x07060302u);
+  p1 = __builtin_amdgcn_perm(u[1][1], u[1][0], 0x07060302u);
+  p2 = __builtin_amdgcn_perm(u[2][1], u[2][0], 0x07060302u);
+}
+// V numbers (a multiple of two) -> V / 2 words of each part.
+template <int V>
+__device__ __forceinline__ void split3(const float (&f)[V], uint32_t (&part)[3][V / 2]) {
+  float probe = 0;
+#pragma unroll
+  for (int j = 0; j < V; j++) probe = fmaf(f[j], 0.0f, probe);  // NaN if any is not finite
+  if (__any(probe != probe)) {
+#pragma unroll
+    for (int j = 0; j < V; j += 2) parts3<true>(f[j], f[j + 1], part[0][j / 2], part[1][j / 2], part[2][j / 2]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; j += 2) parts3<false>(f[j], f[j + 1], part[0][j / 2], part[1][j / 2], part[2][j / 2]);
+  }
+}
+
+// ---- what follows the sum ----
+__device__ __forceinline__ float load_as(const uint8_t* p, int64_t at, int type) {
+  if (type == BQM_F32) return reinterpret_cast<const float*>(p)[at];
+  const uint32_t h = reinterpret_cast<const uint16_t*>(p)[at];
+  return type == BQM_BF16 ? __uint_as_float(h << 16) : (float)__builtin_bit_cast(_Float16, (uint16_t)h);
+}
+__device__ __forceinline__ uint16_t bits16(float v, int type) {
+  if (type == BQM_BF16) return __builtin_bit_cast(uint16_t, (__bf16)v);
+  return __builtin_bit_cast(uint16_t, (_Float16)v);
+}
+__device__ __forceinline__ void store_as(uint8_t* p, int64_t at, float v, int type) {
+  if (type == BQM_F32)
+    reinterpret_cast<float*>(p)[at] = v;
+  else
+    reinterpret_cast<uint16_t*>(p)[at] = bits16(v, type);
+}
+
+// The two gelus are written with the tail of their distribution, which keeps its digits far below 0.
+__device__ __forceinline__ float activate(float z, int act) {
+  switch (act) {
+    case BQM_ACT_RELU: return z < 0.0f ? 0.0f : z;  // a NaN stays
+    case BQM_ACT_SILU: return z / (1.0f + expf(-z));
+    case BQM_ACT_GELU: return 0.5f * z * erfcf(z * -0.70710678f);
+    case BQM_ACT_GELU_TANH: return z / (1.0f + expf(-1.5957691f * (z + 0.044715f * z * z * z)));
+    default: return z;
+  }
+}
+// y of row m (of all rows) and column n, whose group's bias starts at `bias`.
+__device__ __forceinline__ float finish(const Args& a, const float* bias, int64_t m, int64_t n, float z) {
+  if (bias) z += bias[n];
+  z = activate(z, a.act);
+  if (a.mul) z *= load_as(a.mul, m * a.ms + n, a.y_type);
+  if (a.res) z += load_as(a.res, m * a.rs + n, a.y_type);
+  return z;
+}
+
+// ---- groups of rows ----
+struct RowTile {
+  int e, rows;   // group; rows of the tile, 0: no such tile
+  int64_t m0;    // the first of them
+};
+// Row tile `tile` of BM rows, groups ascending, as every thread of a workgroup of NT finds it.  Offsets
+// are kept within the rows, so that whatever they hold, no row outside is touched.  `room`: LDS, free again after
+// the next barrier.
+template <int NT, int BM>
+__device__ __forceinline__ RowTile find_tile(const Args& a, int tile, int64_t (&room)[NT / 64 + 2]) {
+  if (!a.offsets) {
+    const int64_t m0 = (int64_t)tile * BM;
+    return {0, (int)(a.R - m0 < BM ? (a.R - m0 > 0 ? a.R - m0 : 0) : BM), m0};
+  }
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  auto at = [&](int e) {
+    const int64_t o = a.offsets[e];
+    return o < 0 ? (int64_t)0 : o < a.R ? o : a.R;
+  };
+  const int per = (a.E + NT - 1) / NT, e0 = tid * per < a.E ? tid * per : a.E, e1 = e0 + per < a.E ? e0 + per : a.E;
+  auto tiles_of = [&](int64_t lo, int64_t hi) { return hi > lo ? (int)((hi - lo + BM - 1) / BM) : 0; };
+  int mine = 0;
+  int64_t lo = e0 < e1 ? at(e0) : 0;
+  for (int e = e0; e < e1; e++) {
+    const int64_t hi = at(e + 1);
+    mine += tiles_of(lo, hi);
+    lo = hi;
+  }
+  int before = mine;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int u = __shfl_up(before, o, 64);
+    if (lane >= o) before += u;
+  }
+  if (lane == 63) room[wave] = before;
+  if (tid == 0) room[NT / 64] = -1;
+  __syncthreads();
+  before -= mine;
+  for (int k = 0; k < wave; k++) before += (int)room[k];
+  if (tile >= before && tile < before + mine) {
+    lo = at(e0);
+    for (int e = e0; e < e1; e++) {
+      const int64_t hi = at(e + 1);
+      const int k = tiles_of(lo, hi);
+      if (tile < before + k) {
+        room[NT / 64] = e;
+        room[NT / 64 + 1] = lo + (int64_t)(tile - before) * BM;
+        break;
+      }
+      before += k;
+      lo = hi;
+    }
+  }
+  __syncthreads();
+  const int e = __builtin_amdgcn_readfirstlane((int)room[NT / 64]);
+  if (e < 0) return {0, 0, 0};
+  const int64_t m0 = uniform(room[NT / 64 + 1]), left = uniform(at(e + 1)) - m0;
+  return {e, (int)(left < BM ? left : BM), m0};
+}
+
+}  // namespace lin
+}  // namespace bqm

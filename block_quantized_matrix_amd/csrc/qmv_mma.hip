@@ -588,3 +588,4 @@ int launch_id_mma(int fmt, const void* w, const void* w_up, int E, int64_t N, in
 }  // namespace bqm
 
 #include "mxfp4_qmv.h"
+#include "linear_rows.h"

@@ -101,3 +101,4 @@ int launch_unpack(int fmt, const void* src, void* dst, int64_t rows, int64_t K, 
 
 #include "mxfp4_pack.h"
 #include "route.h"
+#include "embed.h"

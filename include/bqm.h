@@ -74,6 +74,10 @@ typedef enum { BQM_Q4_0 = 2, BQM_Q8_0 = 8, BQM_MXFP4 = 39 } bqm_fmt;
 /* Element types of float rows (router logits, the rows of the MXFP4 quantizer). */
 typedef enum { BQM_F32 = 0, BQM_F16 = 1, BQM_BF16 = 30 } bqm_type;
 
+/* Activations of bqm_linear and bqm_linear_grouped: z, max(z, 0), z / (1 + exp(-z)), z times the
+ * normal distribution's share below z, and its tanh form z / (1 + exp(-2 sqrt(2 / pi) (z + 0.044715 z^3))). */
+typedef enum { BQM_ACT_NONE = 0, BQM_ACT_RELU = 1, BQM_ACT_SILU = 2, BQM_ACT_GELU = 3, BQM_ACT_GELU_TANH = 4 } bqm_act;
+
 /* Largest M accepted by qmv_q4_0 / qmv_q8_0, the small-batch decode width. */
 #define BQM_QMV_MAX_M 8
 /* Limits of qmv_id: token count, experts per token, number of experts (the per-expert
@@ -359,6 +363,53 @@ typedef enum { BQM_SOFTMAX = 0, BQM_SIGMOID = 1 } bqm_score;
 int bqm_route(int score, int l_type, const void* logits, int64_t l_stride, const float* bias, int T, int E,
               int n_group, int topk_group, int group_top, int top_k, int renorm, float scale, int32_t* ids,
               float* weights, hipStream_t stream);
+
+/* ---- layers on float rows ---------------------------------------------------------------
+ * What a model does around the products: tokens to rows, and a projection with everything that follows
+ * it up to the next one, on rows as they are (no quantization of activations), in one launch each. */
+
+/* Rows of a packed table by token id, times a scale (the embeddings, which the byte counts of the page
+ * "V100跑Qwen 27B：量化与KV Cache调优，从4到64 tok/s" (lmnt.cn), section 4.1, leave out: gathered, not streamed):
+ *     Y[t][k] = scale * dequant(W)[ids[t]][k]
+ * computed in fp32 and rounded once to y_type.  fmt: any of the three.  w_packed: packed rows x K.  ids:
+ * int32 [T]; a negative id gives a row of zeros, an id >= rows a row of NaN.  Y: [T][K] of y_type with
+ * y_stride >= K elements from row to row, those between rows are left as they are.  MXFP4 weights beyond
+ * fp32's largest number count as they are.  rows, T and K up to 2^30, y_stride too. */
+int bqm_embed(int fmt, const void* w_packed, int64_t rows, int64_t K, const int32_t* ids, int64_t T, float scale,
+              int y_type, void* Y, int64_t y_stride, hipStream_t stream);
+
+/* Linear layer, from one token to long prompts:
+ *     z[m][n] = bias[n] + sum_k dequant(W)[n][k] * X[m][k]
+ *     Y[m][n] = act(z[m][n]) * mul[m][n] + residual[m][n]
+ * fmt: any of the three.  X: [M][K] of x_type.  bias: fp32 [N] or NULL (0).  act: bqm_act.  mul, residual:
+ * [M][N] of y_type, or NULL (1 and 0); mul makes a gated feed-forward's silu(gate) * up of the gate's
+ * product.  Y: [M][N] of y_type; the elements between its rows are left as they are.  mul and residual
+ * may be Y itself (same address and stride), each element is read before it is written.  Rows lie x_stride, mul_stride, res_stride
+ * and y_stride elements apart, at least their length (a stride without a pointer is ignored); X's rows
+ * have to start at multiples of 16 bytes, the others need not.
+ * Arithmetic: codes and rows meet as they are (fp32 rows in three bf16 parts, exact down to a resolution of
+ * 2^-133), block scales in fp32, sums in fp32; one rounding to y_type at the end.  z meets the tolerance of
+ * the products for inputs below 2^116 in magnitude (a block's sum without its scale has to stay a
+ * number of fp32).  K = 0: the sum is 0.  K and x_stride up to BQM_LINEAR_MAX_K, the other strides up to 2^30. */
+#define BQM_LINEAR_MAX_K (1 << 20)
+int bqm_linear(int fmt, const void* w_packed, int x_type, const void* X, int64_t x_stride, const float* bias, int act,
+               const void* mul, int64_t mul_stride, const void* residual, int64_t res_stride, int y_type, void* Y,
+               int64_t y_stride, int64_t M, int64_t N, int64_t K, hipStream_t stream);
+
+/* The linear layer for rows that lie in the order of their experts (the mixture-of-experts layer of the page
+ * "ik_llama.cpp 老工作站多 GPU 部署 Qwen3-235B-A22B 实战指南" (nxmr.cn), background section, after its tokens
+ * were dealt to the experts): rows offsets[e] .. offsets[e + 1] - 1 are expert e's, any number of them, none
+ * too, and take matrix e and bias e:
+ *     z[r][n] = bias[e][n] + sum_k dequant(W)[e][n][k] * X[r][k],   Y as in bqm_linear.
+ * w_packed: expert tensor packed as ONE matrix of E*N rows.  bias: fp32 [E][N] or NULL.  offsets: int32
+ * [E + 1], device memory, not decreasing, from 0 or more up to R or less; rows of Y outside
+ * offsets[0] .. offsets[E] are left as they are.  Offsets below 0 or above R count as 0 or R; where they
+ * decrease, which rows of Y are written, and with what, is not defined (nothing outside Y's R rows is).
+ * E <= BQM_QMV_ID_MAX_E; the rest as bqm_linear with M = R. */
+int bqm_linear_grouped(int fmt, const void* w_packed, int E, const int32_t* offsets, int x_type, const void* X,
+                       int64_t x_stride, const float* bias, int act, const void* mul, int64_t mul_stride,
+                       const void* residual, int64_t res_stride, int y_type, void* Y, int64_t y_stride, int64_t R,
+                       int64_t N, int64_t K, hipStream_t stream);
 
 /* Static English text for a status code. */
 const char* bqm_strerror(int status);
