@@ -116,37 +116,23 @@ __device__ __forceinline__ float scale_from(uint32_t bits) {
 }
 
 // ---- rows as matrix operands ----
-// Pairs of numbers as bf16 parts: each the upper half of what the parts before it leave.  ODD: some are
-// infinite or NaN, of which nothing is left (and a NaN whose payload is in the lower half must stay one).
-template <bool ODD>
-__device__ __forceinline__ void parts3(float a, float b, uint32_t& p0, uint32_t& p1, uint32_t& p2) {
-  float f[2] = {a, b};
-  uint32_t u[3][2];
+// V numbers (a multiple of two) as bf16 parts, V / 2 words of each: a part is the upper half of what the parts
+// before it leave.  Nothing is left of an infinity; what is left of a NaN is one, whose upper half stays one.
+template <int V>
+__device__ __forceinline__ void three_parts(const float (&x)[V], uint32_t (&part)[3][V / 2]) {
 #pragma unroll
-  for (int p = 0; p < 3; p++)
+  for (int j = 0; j < V; j += 2) {
+    uint32_t u[3][2];
 #pragma unroll
     for (int k = 0; k < 2; k++) {
-      u[p][k] = __float_as_uint(f[k]);
-      if (ODD && f[k] != f[k]) u[p][k] |= 0x00400000u;
-      if (p < 2) f[k] -= __uint_as_float(u[p][k] & 0xFFFF0000u);
-      if (ODD && !__builtin_isfinite(f[k])) f[k] = 0;
+      const float f = x[j + k];
+      u[0][k] = __float_as_uint(f);
+      const float g = __builtin_isinf(f) ? 0.0f : f - __uint_as_float(u[0][k] & 0xFFFF0000u);
+      u[1][k] = __float_as_uint(g);
+      u[2][k] = __float_as_uint(g - __uint_as_float(u[1][k] & 0xFFFF0000u));
     }
-  p0 = __builtin_amdgcn_perm(u[0][1], u[0][0], 0x07060302u);
-  p1 = __builtin_amdgcn_perm(u[1][1], u[1][0], 0x07060302u);
-  p2 = __builtin_amdgcn_perm(u[2][1], u[2][0], 0x07060302u);
-}
-// V numbers (a multiple of two) -> V / 2 words of each part.
-template <int V>
-__device__ __forceinline__ void split3(const float (&f)[V], uint32_t (&part)[3][V / 2]) {
-  float probe = 0;
 #pragma unroll
-  for (int j = 0; j < V; j++) probe = fmaf(f[j], 0.0f, probe);  // NaN if any is not finite
-  if (__any(probe != probe)) {
-#pragma unroll
-    for (int j = 0; j < V; j += 2) parts3<true>(f[j], f[j + 1], part[0][j / 2], part[1][j / 2], part[2][j / 2]);
-  } else {
-#pragma unroll
-    for (int j = 0; j < V; j += 2) parts3<false>(f[j], f[j + 1], part[0][j / 2], part[1][j / 2], part[2][j / 2]);
+    for (int p = 0; p < 3; p++) part[p][j / 2] = __builtin_amdgcn_perm(u[p][1], u[p][0], 0x07060302u);
   }
 }
 
@@ -186,65 +172,130 @@ __device__ __forceinline__ float finish(const Args& a, const float* bias, int64_
   return z;
 }
 
+// Four columns from n on, loaded and stored whole (n and the strides are multiples of four).
+__device__ __forceinline__ void load4_as(const uint8_t* p, int64_t at, int type, float (&v)[4]) {
+  if (type == BQM_F32) {
+    const f32x4 u = *reinterpret_cast<const f32x4*>(p + at * 4);
+#pragma unroll
+    for (int j = 0; j < 4; j++) v[j] = u[j];
+  } else {
+    const u32x2 u = *reinterpret_cast<const u32x2*>(p + at * 2);
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      const uint32_t b = u[j >> 1] >> (16 * (j & 1)) & 0xFFFF;
+      v[j] = type == BQM_BF16 ? __uint_as_float(b << 16) : (float)__builtin_bit_cast(_Float16, (uint16_t)b);
+    }
+  }
+}
+__device__ __forceinline__ void finish4(const Args& a, const float* bias, int64_t m, int64_t n, f32x4 z) {
+  float v[4];
+  if (bias)
+#pragma unroll
+    for (int j = 0; j < 4; j++) z[j] += bias[n + j];
+#pragma unroll
+  for (int j = 0; j < 4; j++) z[j] = activate(z[j], a.act);
+  if (a.mul) {
+    load4_as(a.mul, m * a.ms + n, a.y_type, v);
+#pragma unroll
+    for (int j = 0; j < 4; j++) z[j] *= v[j];
+  }
+  if (a.res) {
+    load4_as(a.res, m * a.rs + n, a.y_type, v);
+#pragma unroll
+    for (int j = 0; j < 4; j++) z[j] += v[j];
+  }
+  uint8_t* y = a.y + (m * a.ys + n) * type_size(a.y_type);
+  if (a.y_type == BQM_F32)
+    *reinterpret_cast<f32x4*>(y) = z;
+  else
+    *reinterpret_cast<u32x2*>(y) = u32x2{bits16(z[0], a.y_type) | (uint32_t)bits16(z[1], a.y_type) << 16,
+                                         bits16(z[2], a.y_type) | (uint32_t)bits16(z[3], a.y_type) << 16};
+}
+__device__ __forceinline__ bool by_fours(const Args& a) {
+  return ((a.ys | (a.mul ? a.ms : 0) | (a.res ? a.rs : 0)) & 3) == 0;
+}
+
 // ---- groups of rows ----
 struct RowTile {
   int e, rows;   // group; rows of the tile, 0: no such tile
   int64_t m0;    // the first of them
 };
-// Row tile `tile` of BM rows, groups ascending, as every thread of a workgroup of NT finds it.  Offsets
-// are kept within the rows, so that whatever they hold, no row outside is touched.  `room`: LDS, free again after
-// the next barrier.
+// The row tiles of BM rows, groups ascending, as a workgroup of NT threads counts them (one barrier) and then
+// finds one of them (another).  Offsets are kept within the rows, so that whatever they hold, no row
+// outside is touched.  `room`: LDS, free again after the next barrier.
 template <int NT, int BM>
-__device__ __forceinline__ RowTile find_tile(const Args& a, int tile, int64_t (&room)[NT / 64 + 2]) {
-  if (!a.offsets) {
-    const int64_t m0 = (int64_t)tile * BM;
-    return {0, (int)(a.R - m0 < BM ? (a.R - m0 > 0 ? a.R - m0 : 0) : BM), m0};
-  }
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  auto at = [&](int e) {
+struct RowTiles {
+  const Args& a;
+  int64_t (&room)[NT / 64 + 2];
+  int e0, e1, mine, before, all;
+
+  __device__ __forceinline__ int64_t at(int e) const {
     const int64_t o = a.offsets[e];
     return o < 0 ? (int64_t)0 : o < a.R ? o : a.R;
-  };
-  const int per = (a.E + NT - 1) / NT, e0 = tid * per < a.E ? tid * per : a.E, e1 = e0 + per < a.E ? e0 + per : a.E;
-  auto tiles_of = [&](int64_t lo, int64_t hi) { return hi > lo ? (int)((hi - lo + BM - 1) / BM) : 0; };
-  int mine = 0;
-  int64_t lo = e0 < e1 ? at(e0) : 0;
-  for (int e = e0; e < e1; e++) {
-    const int64_t hi = at(e + 1);
-    mine += tiles_of(lo, hi);
-    lo = hi;
   }
-  int before = mine;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int u = __shfl_up(before, o, 64);
-    if (lane >= o) before += u;
-  }
-  if (lane == 63) room[wave] = before;
-  if (tid == 0) room[NT / 64] = -1;
-  __syncthreads();
-  before -= mine;
-  for (int k = 0; k < wave; k++) before += (int)room[k];
-  if (tile >= before && tile < before + mine) {
-    lo = at(e0);
+  __device__ __forceinline__ static int tiles_of(int64_t lo, int64_t hi) { return hi > lo ? (int)((hi - lo + BM - 1) / BM) : 0; }
+
+  __device__ __forceinline__ RowTiles(const Args& args, int64_t (&lds)[NT / 64 + 2]) : a(args), room(lds) {
+    if (!a.offsets) {
+      all = (int)((a.R + BM - 1) / BM);
+      return;
+    }
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int per = (a.E + NT - 1) / NT;
+    e0 = tid * per < a.E ? tid * per : a.E;
+    e1 = e0 + per < a.E ? e0 + per : a.E;
+    mine = 0;
+    int64_t lo = e0 < e1 ? at(e0) : 0;
     for (int e = e0; e < e1; e++) {
       const int64_t hi = at(e + 1);
-      const int k = tiles_of(lo, hi);
-      if (tile < before + k) {
-        room[NT / 64] = e;
-        room[NT / 64 + 1] = lo + (int64_t)(tile - before) * BM;
-        break;
-      }
-      before += k;
+      mine += tiles_of(lo, hi);
       lo = hi;
     }
+    before = mine;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int u = __shfl_up(before, o, 64);
+      if (lane >= o) before += u;
+    }
+    if (lane == 63) room[wave] = before;
+    if (tid == 0) room[NT / 64] = -1;
+    __syncthreads();
+    before -= mine;
+    all = 0;
+    for (int k = 0; k < NT / 64; k++) {
+      const int n = __builtin_amdgcn_readfirstlane((int)room[k]);
+      if (k < wave) before += n;
+      all += n;
+    }
   }
-  __syncthreads();
-  const int e = __builtin_amdgcn_readfirstlane((int)room[NT / 64]);
-  if (e < 0) return {0, 0, 0};
-  const int64_t m0 = uniform(room[NT / 64 + 1]), left = uniform(at(e + 1)) - m0;
-  return {e, (int)(left < BM ? left : BM), m0};
-}
+
+  __device__ __forceinline__ RowTile find(int tile) {
+    if (!a.offsets) {
+      const int64_t m0 = (int64_t)tile * BM, left = a.R - m0;
+      return {0, (int)(left < BM ? (left > 0 ? left : 0) : BM), m0};
+    }
+    if (tile >= before && tile < before + mine) {
+      int first = before;
+      int64_t lo = at(e0);
+      for (int e = e0; e < e1; e++) {
+        const int64_t hi = at(e + 1);
+        const int k = tiles_of(lo, hi);
+        if (tile < first + k) {
+          room[NT / 64] = e;
+          room[NT / 64 + 1] = lo + (int64_t)(tile - first) * BM;
+          break;
+        }
+        first += k;
+        lo = hi;
+      }
+    }
+    __syncthreads();
+    const int e = __builtin_amdgcn_readfirstlane((int)room[NT / 64]);
+    if (e < 0) return {0, 0, 0};
+    const int64_t m0 = uniform(room[NT / 64 + 1]), left = uniform(at(e + 1)) - m0;
+    return {e, (int)(left < BM ? left : BM), m0};
+  }
+};
 
 }  // namespace lin
 }  // namespace bqm

@@ -31,7 +31,7 @@ __global__ __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(OCC, OCC
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i = lane & 15, q = lane >> 4;
   const int tile = blockIdx.x / span, run = blockIdx.x - tile * span;
-  const RowTile at = find_tile<W * 64, RM>(a, tile, room);
+  const RowTile at = RowTiles<W * 64, RM>(a, room).find(tile);
   if (at.rows <= 0) return;  // the whole workgroup
   const int64_t r0 = (int64_t)run * halves * 8, r1 = r0 + halves * 8 < a.N ? r0 + halves * 8 : a.N;
   const int64_t w0 = at.e * a.N + r0;  // the first weight row, of all matrices
@@ -101,7 +101,7 @@ __global__ __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(OCC, OCC
         const int c = lane & 7;  // four numbers of block `block`
         const float f[4] = {__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]), __uint_as_float(v[3])};
         uint32_t part[3][2];
-        split3<4>(f, part);
+        three_parts<4>(f, part);
         if (m < RM)
 #pragma unroll
           for (int p = 0; p < 3; p++) {
@@ -291,7 +291,8 @@ int launch_linear(int fmt, const void* w, int E, const int32_t* offsets, int x_t
     a.scales_off = L.scales_off;
   }
   const int64_t groups = offsets ? (E < R ? E : R) : 1;
-  return launch_linear_rows(fmt, x_type, a, groups, (R + groups - 1) / groups, s);
+  const int64_t each = (R + groups - 1) / groups;
+  return each > 64 ? launch_linear_tiles(fmt, x_type, a, groups, each, s) : launch_linear_rows(fmt, x_type, a, groups, each, s);
 }
 
 }  // namespace bqm

@@ -661,3 +661,4 @@ int launch_qmm_id(int fmt, const void* w, int E, int64_t N, int64_t K, const int
 }  // namespace bqm
 
 #include "mxfp4_qmm.h"
+#include "linear_tiles.h"
