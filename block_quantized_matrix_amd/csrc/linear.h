@@ -41,13 +41,15 @@ constexpr uint32_t kOob = 0x80000000u;  // an offset past every descriptor: read
 __host__ __device__ constexpr int type_size(int type) { return type == BQM_F32 ? 4 : 2; }
 constexpr int parts_of(int type) { return type == BQM_F32 ? 3 : 1; }
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p, int64_t bytes) {
-  const int64_t most = 0x7FFFFFFF;
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)(bytes < 0 ? 0 : bytes < most ? bytes : most), 0x00020000);
-}
-
 __device__ __forceinline__ int64_t uniform(int64_t v) {
   return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32 | (uint32_t)__builtin_amdgcn_readfirstlane((int)v));
+}
+
+// (Where it does not see that a descriptor is the same in all lanes, the compiler loops over them at each load.)
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p, int64_t bytes) {
+  const int64_t most = 0x7FFFFFFF;
+  return __builtin_amdgcn_make_buffer_rsrc((void*)uniform((int64_t)p), 0,
+                                           __builtin_amdgcn_readfirstlane((int)(bytes < 0 ? 0 : bytes < most ? bytes : most)), 0x00020000);
 }
 
 // ---- codes as matrix operands ----
@@ -154,62 +156,93 @@ __device__ __forceinline__ void store_as(uint8_t* p, int64_t at, float v, int ty
 }
 
 // The two gelus are written with the tail of their distribution, which keeps its digits far below 0.
-__device__ __forceinline__ float activate(float z, int act) {
-  switch (act) {
-    case BQM_ACT_RELU: return z < 0.0f ? 0.0f : z;  // a NaN stays
-    case BQM_ACT_SILU: return z / (1.0f + expf(-z));
-    case BQM_ACT_GELU: return 0.5f * z * erfcf(z * -0.70710678f);
-    case BQM_ACT_GELU_TANH: return z / (1.0f + expf(-1.5957691f * (z + 0.044715f * z * z * z)));
-    default: return z;
+template <int V>
+__device__ __forceinline__ void activate(float (&z)[V], int act) {
+  if (act == BQM_ACT_RELU) {
+#pragma unroll
+    for (int j = 0; j < V; j++) z[j] = z[j] < 0.0f ? 0.0f : z[j];  // a NaN stays
+  } else if (act == BQM_ACT_SILU) {
+#pragma unroll
+    for (int j = 0; j < V; j++) z[j] = z[j] / (1.0f + expf(-z[j]));
+  } else if (act == BQM_ACT_GELU) {
+#pragma unroll
+    for (int j = 0; j < V; j++) z[j] = 0.5f * z[j] * erfcf(z[j] * -0.70710678f);
+  } else if (act == BQM_ACT_GELU_TANH) {
+#pragma unroll
+    for (int j = 0; j < V; j++) z[j] = z[j] / (1.0f + expf(-1.5957691f * (z[j] + 0.044715f * z[j] * z[j] * z[j])));
   }
 }
 // y of row m (of all rows) and column n, whose group's bias starts at `bias`.
-__device__ __forceinline__ float finish(const Args& a, const float* bias, int64_t m, int64_t n, float z) {
-  if (bias) z += bias[n];
-  z = activate(z, a.act);
-  if (a.mul) z *= load_as(a.mul, m * a.ms + n, a.y_type);
-  if (a.res) z += load_as(a.res, m * a.rs + n, a.y_type);
-  return z;
+__device__ __forceinline__ float finish(const Args& a, const float* bias, int64_t m, int64_t n, float sum) {
+  float z[1] = {bias ? sum + bias[n] : sum};
+  activate(z, a.act);
+  if (a.mul) z[0] *= load_as(a.mul, m * a.ms + n, a.y_type);
+  if (a.res) z[0] += load_as(a.res, m * a.rs + n, a.y_type);
+  return z[0];
 }
-
-// Four columns from n on, loaded and stored whole (n and the strides are multiples of four).
-__device__ __forceinline__ void load4_as(const uint8_t* p, int64_t at, int type, float (&v)[4]) {
-  if (type == BQM_F32) {
-    const f32x4 u = *reinterpret_cast<const f32x4*>(p + at * 4);
+// Four columns from n on in each of R rows (m, m + step, ...; those from `end` on are left out), loaded and
+// stored whole where n + 4 <= N and the strides are multiples of four.
+template <int R>
+__device__ __forceinline__ void finish4(const Args& a, const f32x4& bias, int64_t m, int step, int64_t end, int64_t n, const f32x4 (&sum)[R]) {
+  float z[R * 4];
 #pragma unroll
-    for (int j = 0; j < 4; j++) v[j] = u[j];
-  } else {
-    const u32x2 u = *reinterpret_cast<const u32x2*>(p + at * 2);
+  for (int r = 0; r < R; r++)
 #pragma unroll
-    for (int j = 0; j < 4; j++) {
-      const uint32_t b = u[j >> 1] >> (16 * (j & 1)) & 0xFFFF;
-      v[j] = type == BQM_BF16 ? __uint_as_float(b << 16) : (float)__builtin_bit_cast(_Float16, (uint16_t)b);
+    for (int j = 0; j < 4; j++) z[r * 4 + j] = sum[r][j] + bias[j];
+  const int size = a.y_type == BQM_F32 ? 4 : 2;
+  auto loaded = [&](const uint8_t* p, int64_t stride, auto&& use) {
+    if (size == 4) {
+      f32x4 u[R];
+#pragma unroll
+      for (int r = 0; r < R; r++)
+        if (m + r * step < end) u[r] = *reinterpret_cast<const f32x4*>(p + ((m + r * step) * stride + n) * 4);
+#pragma unroll
+      for (int r = 0; r < R; r++)
+#pragma unroll
+        for (int j = 0; j < 4; j++) use(z[r * 4 + j], u[r][j]);
+      return;
     }
+    u32x2 u[R];
+#pragma unroll
+    for (int r = 0; r < R; r++)
+      if (m + r * step < end) u[r] = *reinterpret_cast<const u32x2*>(p + ((m + r * step) * stride + n) * 2);
+    if (a.y_type == BQM_BF16) {
+#pragma unroll
+      for (int r = 0; r < R; r++)
+#pragma unroll
+        for (int j = 0; j < 4; j++) use(z[r * 4 + j], __uint_as_float(j & 1 ? u[r][j >> 1] & 0xFFFF0000u : u[r][j >> 1] << 16));
+    } else {
+#pragma unroll
+      for (int r = 0; r < R; r++)
+#pragma unroll
+        for (int j = 0; j < 4; j++) use(z[r * 4 + j], (float)__builtin_bit_cast(_Float16, (uint16_t)(u[r][j >> 1] >> (16 * (j & 1)))));
+    }
+  };
+  activate(z, a.act);
+  if (a.mul) loaded(a.mul, a.ms, [](float& v, float u) { v *= u; });
+  if (a.res) loaded(a.res, a.rs, [](float& v, float u) { v += u; });
+  if (size == 4) {
+#pragma unroll
+    for (int r = 0; r < R; r++)
+      if (m + r * step < end)
+        *reinterpret_cast<f32x4*>(a.y + ((m + r * step) * a.ys + n) * 4) = f32x4{z[r * 4], z[r * 4 + 1], z[r * 4 + 2], z[r * 4 + 3]};
+    return;
   }
-}
-__device__ __forceinline__ void finish4(const Args& a, const float* bias, int64_t m, int64_t n, f32x4 z) {
-  float v[4];
-  if (bias)
+  u32x2 u[R];
+  if (a.y_type == BQM_BF16) {
 #pragma unroll
-    for (int j = 0; j < 4; j++) z[j] += bias[n + j];
+    for (int r = 0; r < R; r++)
 #pragma unroll
-  for (int j = 0; j < 4; j++) z[j] = activate(z[j], a.act);
-  if (a.mul) {
-    load4_as(a.mul, m * a.ms + n, a.y_type, v);
+      for (int j = 0; j < 2; j++) u[r][j] = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)z[r * 4 + 2 * j], (__bf16)z[r * 4 + 2 * j + 1]});
+  } else {
 #pragma unroll
-    for (int j = 0; j < 4; j++) z[j] *= v[j];
+    for (int r = 0; r < R; r++)
+#pragma unroll
+      for (int j = 0; j < 2; j++) u[r][j] = __builtin_bit_cast(uint32_t, f16x2{(_Float16)z[r * 4 + 2 * j], (_Float16)z[r * 4 + 2 * j + 1]});
   }
-  if (a.res) {
-    load4_as(a.res, m * a.rs + n, a.y_type, v);
 #pragma unroll
-    for (int j = 0; j < 4; j++) z[j] += v[j];
-  }
-  uint8_t* y = a.y + (m * a.ys + n) * type_size(a.y_type);
-  if (a.y_type == BQM_F32)
-    *reinterpret_cast<f32x4*>(y) = z;
-  else
-    *reinterpret_cast<u32x2*>(y) = u32x2{bits16(z[0], a.y_type) | (uint32_t)bits16(z[1], a.y_type) << 16,
-                                         bits16(z[2], a.y_type) | (uint32_t)bits16(z[3], a.y_type) << 16};
+  for (int r = 0; r < R; r++)
+    if (m + r * step < end) *reinterpret_cast<u32x2*>(a.y + ((m + r * step) * a.ys + n) * 2) = u[r];
 }
 __device__ __forceinline__ bool by_fours(const Args& a) {
   return ((a.ys | (a.mul ? a.ms : 0) | (a.res ? a.rs : 0)) & 3) == 0;

@@ -18,21 +18,22 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 // Four waves side by side along the weight rows (TN tiles of 32 each), all over the same TM tiles of 32 rows.
 // K advances by steps of two blocks.  The rows go from memory straight into LDS, four stages, three steps
 // ahead; codes and scales straight to the registers of the wave that converts them, D steps ahead.
-template <int FMT, int XT, int TN, int TM>
+template <int FMT, int XT, int NW, int TN, int TM>
 struct LinTile {
-  static constexpr int kWaves = 4, kBN = kWaves * TN * 32, kBM = TM * 32;
+  static constexpr int kWaves = NW, kBN = kWaves * TN * 32, kBM = TM * 32;
   static constexpr int kXB = lin::type_size(XT), kRow = 64 * kXB;  // bytes of a row's step
   static constexpr int kStage = kBM * kRow, kPieces = kStage / (kWaves * 1024);
   static constexpr int kLoads = FMT == BQM_Q8_0 ? 2 : 1;           // of 16 bytes a lane, of a weight tile's step
+  static_assert(TN <= 2, "a lane for each of a wave's rows");
   static_assert(kStage % (kWaves * 1024) == 0, "whole loads");
 };
 
-template <int FMT, int XT, int TN, int TM>
+template <int FMT, int XT, int NW, int TN, int TM>
 __device__ __forceinline__ void lin_core(const lin::Args& a, const lin::RowTile& at, int tn, uint8_t* lds0, uint8_t* lds1, uint8_t* lds2,
-                                         uint8_t* lds3) {
+                                         uint8_t* lds3, uint8_t* scales) {
   using namespace lin;
-  using C = LinTile<FMT, XT, TN, TM>;
-  constexpr int P = parts_of(XT), L = C::kLoads, PX = C::kPieces, D = 2;
+  using C = LinTile<FMT, XT, NW, TN, TM>;
+  constexpr int P = parts_of(XT), L = C::kLoads, PX = C::kPieces;
   constexpr bool MX = FMT == BQM_MXFP4;
   constexpr int CB = FMT == BQM_Q8_0 ? 32 : 16;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -48,52 +49,70 @@ __device__ __forceinline__ void lin_core(const lin::Args& a, const lin::RowTile&
   const int own = left > 0 ? left : 1;
   const int64_t span = ((first & 15) + own + 15) >> 4;
   const __amdgpu_buffer_rsrc_t rc = rsrc(wc, MX ? span * a.ks * mx::kOperand : (int64_t)own * nb * CB);
-  const __amdgpu_buffer_rsrc_t rd = rsrc(wd, MX ? span * a.kg * mx::kScaleTile : (int64_t)own * nb * 2 + 2);  // a word at the last scale
-  uint32_t oc[TN], od[TN];
+  const __amdgpu_buffer_rsrc_t rd = rsrc(wd, MX ? span * a.kg * mx::kScaleTile : (int64_t)own * nb * 2 + 14);  // sixteen bytes at the last scale
+  // Loads past the last again take what the last one takes (a branch around a load would make the compiler
+  // wait for all loads where the paths join).
+  uint32_t oc[TN];
 #pragma unroll
   for (int t = 0; t < TN; t++) {
-    const int r = t * 32 + i < own ? t * 32 + i : own - 1, mr = (int)(first & 15) + r;
-    if (MX)
-      oc[t] = (uint32_t)mx::code_at(mr, h, a.ks), od[t] = (uint32_t)((mr >> 4) * a.kg * mx::kScaleTile + h * 64 + (mr & 15) * 4);
-    else
-      oc[t] = (uint32_t)(r * nb * CB + h * 16), od[t] = (uint32_t)(r * nb * 2);
+    const int r = t * 32 + i < own ? t * 32 + i : own - 1;
+    oc[t] = MX ? (uint32_t)mx::code_at((first & 15) + r, h, a.ks) : (uint32_t)(r * nb * CB + h * 16);
   }
-  // Every step loads, those past the last again what the last one takes (a branch around a load would make
-  // the compiler wait for all loads where the paths join).
-  u32x4 code[D][TN][L];
-  uint32_t scale[D][TN];
-  auto load_w = [&](int d, int s) {
-    s = s < steps ? s : steps - 1;
+  u32x4 code[2][TN];  // of two blocks of Q8_0 each, two steps of the others
+  auto load_codes = [&](int d, int u) {
+    const int most = L == 2 ? nb - 1 : steps - 1;
+    u = u < most ? u : most;
+    const int at = MX ? (u >> 1) * mx::kOperand + (u & 1) * 512 : u * 32;
 #pragma unroll
-    for (int t = 0; t < TN; t++) {
+    for (int t = 0; t < TN; t++) code[d][t] = __builtin_amdgcn_raw_buffer_load_b128(rc, oc[t], at, 0);
+  };
+  // Scales: lane l brings those of row l and four steps (16 bytes) to LDS of the wave's own.
+  uint32_t od;
+  {
+    const int r = lane < own ? lane : own - 1, mr = (int)(first & 15) + r;
+    od = MX ? (uint32_t)((mr >> 4) * a.kg * mx::kScaleTile + (mr & 15) * 4) : (uint32_t)(r * nb * 2);
+  }
+  u32x4 fresh;
+  auto load_scales = [&](int g) {  // of steps 4 g .. 4 g + 3
+    if constexpr (MX) {  // a word: four blocks, four apart
+      const int most = (steps - 1) >> 3, at = (g >> 1 < most ? g >> 1 : most) * mx::kScaleTile;
 #pragma unroll
-      for (int l = 0; l < L; l++)
-        code[d][t][l] = __builtin_amdgcn_raw_buffer_load_b128(rc, oc[t] + l * 32, MX ? (s >> 1) * mx::kOperand + (s & 1) * 512 : s * 2 * CB, 0);
-      if constexpr (MX)  // of one of the two blocks
-        scale[d][t] = __builtin_amdgcn_raw_buffer_load_b8(rd, od[t], (s >> 3) * mx::kScaleTile + (s & 1) * 128 + (s >> 1 & 3), 0);
-      else  // of both
-        scale[d][t] = __builtin_amdgcn_raw_buffer_load_b32(rd, od[t], s * 4, 0);
+      for (int k = 0; k < 4; k++) fresh[k] = __builtin_amdgcn_raw_buffer_load_b32(rd, od + k * 64, at, 0);
+    } else {
+      const int most = (steps - 1) >> 2;
+      fresh = __builtin_amdgcn_raw_buffer_load_b128(rd, od, (g < most ? g : most) * 16, 0);
     }
   };
+  uint8_t* sc = scales + wave * 2 * 1024;
+  auto keep_scales = [&](int g) { *reinterpret_cast<u32x4*>(sc + (g & 1) * 1024 + lane * 16) = fresh; };
+  auto scale_at = [&](int t, int s, int b) {  // of block b of step s
+    const uint8_t* p = sc + (s >> 2 & 1) * 1024 + (t * 32 + i) * 16;
+    if constexpr (MX) return (uint32_t)p[((s & 1) * 2 + b) * 4 + (s >> 1 & 3)];
+    return (uint32_t)reinterpret_cast<const uint16_t*>(p)[(s & 3) * 2 + b];
+  };
 
-  // rows: 16-byte slots, that of place p in row m holding slot p ^ (m & 7), so that lanes a row apart read
-  // other banks
+  // rows: 16-byte slots, place p of row m holding slot p ^ turned(m): the sixteen lanes that LDS serves
+  // at a time, a row apart each, find their slots in all 64 banks
   const __amdgpu_buffer_rsrc_t rx = rsrc(a.x + at.m0 * a.xs, (int64_t)(at.rows - 1) * a.xs + (int64_t)nb * 32 * C::kXB);
-  constexpr int kSlots = C::kRow / 16;
+  constexpr int kSlots = C::kRow / 16;  // 8, or 16 of fp32
+  auto turned = [](int m) { return kSlots == 8 ? m >> 1 & 7 : m & 15; };
   uint32_t ox[PX];
 #pragma unroll
   for (int p = 0; p < PX; p++) {
-    const int u = (p * 4 + wave) * 64 + lane, m = u / kSlots, slot = u % kSlots ^ (m & 7);
+    const int u = (p * NW + wave) * 64 + lane, m = u / kSlots, slot = (u % kSlots ^ turned(m)) & (nb > 1 ? kSlots - 1 : kSlots / 2 - 1);
     ox[p] = (uint32_t)((m < at.rows ? m : at.rows - 1) * (int)a.xs + slot * 16);
   }
+  // The last step of an odd number of blocks takes the last two (of a single block: that block twice), so that
+  // nothing is read past a row.
   auto load_x = [&](int s, uint8_t* stage) {
     s = s < steps ? s : steps - 1;
+    const int at = 2 * s + 2 <= nb || nb == 1 ? 2 * s : nb - 2;
 #pragma unroll
     for (int p = 0; p < PX; p++)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (LdsPtr)(stage + (p * 4 + wave) * 1024), 16, ox[p], s * C::kRow, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (LdsPtr)(stage + (p * NW + wave) * 1024), 16, ox[p], at * (C::kRow / 2), 0, 0);
   };
   auto slot_at = [&](const uint8_t* stage, int t, int slot) {
-    return *reinterpret_cast<const u32x4*>(stage + (t * 32 + i) * C::kRow + (slot ^ (i & 7)) * 16);
+    return *reinterpret_cast<const u32x4*>(stage + (t * 32 + i) * C::kRow + (slot ^ turned(i)) * 16);
   };
 
   f32x16 acc[TN][TM] = {};
@@ -102,161 +121,233 @@ __device__ __forceinline__ void lin_core(const lin::Args& a, const lin::RowTile&
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   };
-  auto block = [&](int d, int b, const uint8_t* stage) {
-    // the codes of block b: of each tile, first half and second half of its k
-    u32x4 w[TN][2];
-    float f[TN];
-#pragma unroll
-    for (int t = 0; t < TN; t++) {
-      u32x4 v = code[d][t][FMT == BQM_Q8_0 ? b : 0];
-      // the halves of a wave loaded a unit each; now each has its half of both
-      uint32_t v0 = v[0], v1 = v[1], v2 = v[2], v3 = v[3];
-      mma::swap32(v0, v2);
-      mma::swap32(v1, v3);
-      if constexpr (FMT == BQM_Q8_0) {
-        uint32_t u[4][2];
-        bytes<XT>(v0, u[0]);
-        bytes<XT>(v1, u[1]);
-        bytes<XT>(v2, u[2]);
-        bytes<XT>(v3, u[3]);
-        w[t][0] = u32x4{u[0][0], u[0][1], u[1][0], u[1][1]};
-        w[t][1] = u32x4{u[2][0], u[2][1], u[3][0], u[3][1]};
-      } else {
-        uint32_t lo[2][2], hi[2][2];
-        nibbles<FMT, XT>(b ? v2 : v0, lo[0], hi[0]);
-        nibbles<FMT, XT>(b ? v3 : v1, lo[1], hi[1]);
-        w[t][0] = u32x4{lo[0][0], lo[0][1], lo[1][0], lo[1][1]};
-        w[t][1] = u32x4{hi[0][0], hi[0][1], hi[1][0], hi[1][1]};
-      }
-      uint32_t s0 = scale[d][t], s1 = s0;
-      if constexpr (MX)
-        mma::swap32(s0, s1);
-      else
-        s1 >>= 16;
-      f[t] = scale_from<FMT, XT>(b ? s1 : s0);
-    }
-#pragma unroll
-    for (int m = 0; m < TM; m++) {
-      u32x4 x[2][P];
+  // Matrix operands of block b of step s from the codes: of each weight tile the two halves of its k.  (The
+  // lane halves hold a unit of 16 bytes each.  A unit of Q8_0 is half a block: lanes h take k = 16 h + 8 j ..
+  // of half j.  One of nibbles is a block: halves of units are exchanged, then lanes h hold k = 8 h .. of the
+  // low nibbles and 16 + 8 h .. of the high ones.)
+  auto convert = [&](int b, int d, int t, uint32_t scale, u32x4 (&w)[2], float& f) {
+    u32x4& v = code[d][t];
+    if constexpr (FMT == BQM_Q8_0) {
 #pragma unroll
       for (int j = 0; j < 2; j++) {
-        if constexpr (P == 1) {
-          x[j][0] = slot_at(stage, m, b * 4 + j * 2 + h);
-        } else {
-          const u32x4 v0 = slot_at(stage, m, b * 8 + j * 4 + h * 2), v1 = slot_at(stage, m, b * 8 + j * 4 + h * 2 + 1);
-          float g[8];
-#pragma unroll
-          for (int k = 0; k < 4; k++) g[k] = __uint_as_float(v0[k]), g[4 + k] = __uint_as_float(v1[k]);
-          uint32_t part[3][4];
-          three_parts<8>(g, part);
-#pragma unroll
-          for (int p = 0; p < 3; p++) x[j][p] = u32x4{part[p][0], part[p][1], part[p][2], part[p][3]};
-        }
+        uint32_t u[2][2];
+        bytes<XT>(v[2 * j], u[0]);
+        bytes<XT>(v[2 * j + 1], u[1]);
+        w[j] = u32x4{u[0][0], u[0][1], u[1][0], u[1][1]};
       }
+    } else {
+      if (b == 0) {
+        uint32_t v0 = v[0], v1 = v[1], v2 = v[2], v3 = v[3];
+        mma::swap32(v0, v2);
+        mma::swap32(v1, v3);
+        v = u32x4{v0, v1, v2, v3};
+      }
+      uint32_t lo[2][2], hi[2][2];
+      nibbles<FMT, XT>(v[2 * b], lo[0], hi[0]);
+      nibbles<FMT, XT>(v[2 * b + 1], lo[1], hi[1]);
+      w[0] = u32x4{lo[0][0], lo[0][1], lo[1][0], lo[1][1]};
+      w[1] = u32x4{hi[0][0], hi[0][1], hi[1][0], hi[1][1]};
+    }
+    f = scale_from<FMT, XT>(scale);
+    asm volatile("" : "+v"(w[0]), "+v"(w[1]), "+v"(f));  // here, not where the next block uses them
+  };
+  auto rows_of = [&](const uint8_t* stage, int m, int b, u32x4 (&x)[2][P]) {
 #pragma unroll
-      for (int t = 0; t < TN; t++) {
-        f32x16 sum{};
+    for (int j = 0; j < 2; j++) {
+      const int eight = b * 4 + (FMT == BQM_Q8_0 ? h * 2 + j : j * 2 + h);  // of the step's lots of eight k
+      if constexpr (P == 1) {
+        x[j][0] = slot_at(stage, m, eight);
+      } else {
+        const u32x4 v0 = slot_at(stage, m, eight * 2), v1 = slot_at(stage, m, eight * 2 + 1);
+        float g[8];
 #pragma unroll
-        for (int j = 0; j < 2; j++)
+        for (int e = 0; e < 4; e++) g[e] = __uint_as_float(v0[e]), g[4 + e] = __uint_as_float(v1[e]);
+        uint32_t part[3][4];
+        three_parts<8>(g, part);
 #pragma unroll
-          for (int p = 0; p < P; p++) {
-            if constexpr (XT == BQM_F16)
-              sum = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, x[j][p]), __builtin_bit_cast(f16x8, w[t][j]), sum, 0, 0, 0);
-            else
-              sum = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, x[j][p]), __builtin_bit_cast(bf16x8, w[t][j]), sum, 0, 0, 0);
-          }
-#pragma unroll
-        for (int r = 0; r < 16; r++) acc[t][m][r] = fmaf(f[t], sum[r], acc[t][m][r]);
+        for (int p = 0; p < 3; p++) x[j][p] = u32x4{part[p][0], part[p][1], part[p][2], part[p][3]};
       }
     }
   };
-  auto step = [&](int d, int s, uint8_t* cur, uint8_t* free) {
-    // x of step s was issued before the weights of s + D - 1 .. and the rows of s + 1, s + 2
-    vm_wait<2 * (PX + TN * (L + 1))>();
-    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave has read all of the stage that is free now
-    meet();
-    __builtin_amdgcn_sched_barrier(0);
-    load_x(s + 3, free);
-    __builtin_amdgcn_sched_barrier(0);
-    block(d, 0, cur);
-    if (2 * s + 1 < nb) block(d, 1, cur);
-    __builtin_amdgcn_sched_barrier(0);
-    load_w(d, s + D);
+  auto products = [&](const u32x4 (&x)[2][P], const u32x4 (&w)[2]) {
+    f32x16 sum{};
+#pragma unroll
+    for (int j = 0; j < 2; j++)
+#pragma unroll
+      for (int p = 0; p < P; p++) {
+        if constexpr (XT == BQM_F16)
+          sum = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, x[j][p]), __builtin_bit_cast(f16x8, w[j]), sum, 0, 0, 0);
+        else
+          sum = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, x[j][p]), __builtin_bit_cast(bf16x8, w[j]), sum, 0, 0, 0);
+      }
+    return sum;
+  };
+  auto add_scaled = [&](f32x16& to, const f32x16& sum, float f) {
+#pragma unroll
+    for (int r = 0; r < 16; r++) to[r] = fmaf(f, sum[r], to[r]);
+  };
+  // Blocks in a pipeline: beside a pair of tiles' products stand the scaling of the pair before, the reading of
+  // the next rows as soon as the last product has taken these, and likewise the conversion of the next block.
+  constexpr int K = TM * TN;
+  u32x4 w[TN][2], x[2][P];
+  float f[TN], f_last;
+  f32x16 sum[2];
+  auto block = [&](auto bc, int s, int next_d, const uint8_t* stage, const uint8_t* next_stage, auto&& between) {
+    constexpr int B = decltype(bc)::value;
+    float g[TN];
+    uint32_t bits[TN];
+#pragma unroll
+    for (int k = 0; k < K; k++) {
+      const int m = k / TN, t = k % TN;
+      if (k == K / 2) between();
+      sum[k & 1] = products(x, w[t]);
+      if (t == TN - 1) {
+        if (m + 1 < TM)
+          rows_of(stage, m + 1, B, x);
+        else
+          rows_of(next_stage, 0, B ^ 1, x);
+      }
+      if (k > 0)
+        add_scaled(acc[(k - 1) % TN][(k - 1) / TN], sum[(k - 1) & 1], f[(k - 1) % TN]);
+      else if (B == 1)
+        add_scaled(acc[TN - 1][TM - 1], sum[(K - 1) & 1], f_last);
+      if (m == TM - 2) bits[t] = scale_at(t, B ? s + 1 : s, B ^ 1);
+      if (m == TM - 1) convert(B ^ 1, next_d, t, bits[t], w[t], g[t]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (B == 1) add_scaled(acc[TN - 1][TM - 1], sum[(K - 1) & 1], f[TN - 1]);
+    f_last = f[TN - 1];
+#pragma unroll
+    for (int t = 0; t < TN; t++) f[t] = g[t];
+  };
+  // The Q-th step of four; whole steps, both blocks.
+  auto step = [&](auto qc, int s, const uint8_t* cur, const uint8_t* nxt, uint8_t* free) {
+    constexpr int Q = decltype(qc)::value, d = Q & 1;
+    // codes: block 0 converts block 1 of this step, block 1 block 0 of the next
+    block(std::integral_constant<int, 0>{}, s, L == 2 ? 1 : d, cur, cur, [] {});
+    load_codes(L == 2 ? 1 : d, L == 2 ? 2 * s + 3 : s + 2);
+    if constexpr (Q == 0) load_scales((s >> 2) + 1);
+    if constexpr (Q == 3) {  // the next step's are asked for in the block that follows
+      keep_scales((s >> 2) + 1);
+      mx::wave_turn();
+    }
+    if constexpr (L == 1) __builtin_amdgcn_sched_barrier(0);
+    block(std::integral_constant<int, 1>{}, s, L == 2 ? 0 : d ^ 1, cur, nxt, [&] {
+      // the rows of step s + 1 have arrived, and every wave has read all of step s - 1
+      vm_wait<PX + TN>();
+      meet();
+      load_x(s + 3, free);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    if constexpr (L == 2) load_codes(0, 2 * s + 4);
     __builtin_amdgcn_sched_barrier(0);
   };
+  const int whole = nb >> 1;
   if (steps > 0) {
+    load_scales(0);
+    load_codes(0, 0);
+    load_codes(1, 1);
+    __builtin_amdgcn_sched_barrier(0);
     load_x(0, lds0);
-    __builtin_amdgcn_sched_barrier(0);
-    load_w(0, 0);
-    __builtin_amdgcn_sched_barrier(0);
     load_x(1, lds1);
-    __builtin_amdgcn_sched_barrier(0);
-    load_w(1, 1);
-    __builtin_amdgcn_sched_barrier(0);
     load_x(2, lds2);
+    keep_scales(0);
+    mx::wave_turn();
+    vm_wait<0>();
+    meet();
+    rows_of(lds0, 0, 0, x);
+#pragma unroll
+    for (int t = 0; t < TN; t++) convert(0, 0, t, scale_at(t, 0, 0), w[t], f[t]);
+    if constexpr (L == 2) load_codes(0, 2);
     __builtin_amdgcn_sched_barrier(0);
-    for (int s = 0;; s += 4) {
-      step(0, s, lds0, lds3);
-      if (s + 1 >= steps) break;
-      step(1, s + 1, lds1, lds0);
-      if (s + 2 >= steps) break;
-      step(0, s + 2, lds2, lds1);
-      if (s + 3 >= steps) break;
-      step(1, s + 3, lds3, lds2);
-      if (s + 4 >= steps) break;
+    for (int s = 0; s < whole; s += 4) {
+      step(std::integral_constant<int, 0>{}, s, lds0, lds1, lds3);
+      if (s + 1 >= whole) break;
+      step(std::integral_constant<int, 1>{}, s + 1, lds1, lds2, lds0);
+      if (s + 2 >= whole) break;
+      step(std::integral_constant<int, 2>{}, s + 2, lds2, lds3, lds1);
+      if (s + 3 >= whole) break;
+      step(std::integral_constant<int, 3>{}, s + 3, lds3, lds0, lds2);
+    }
+    if (nb & 1) {  // a last block without a partner, its codes already at hand
+      const uint8_t* stage = (whole & 3) == 0 ? lds0 : (whole & 3) == 1 ? lds1 : (whole & 3) == 2 ? lds2 : lds3;
+#pragma unroll
+      for (int m = 0; m < TM; m++) {
+        rows_of(stage, m, nb > 1, x);
+#pragma unroll
+        for (int t = 0; t < TN; t++) add_scaled(acc[t][m], products(x, w[t]), f[t]);
+      }
     }
   }
   vm_wait<0>();  // nothing may be on its way into LDS when it is used again
   __syncthreads();
   // A lane holds column i of a weight tile, rows 8 (r / 4) + 4 h + r % 4 of a row tile.  Each wave turns its row
   // tiles in a stage of its own, so that it stores whole runs of a row of Y.
-  constexpr int kCols = TN * 32;
-  static_assert(32 * kCols * 4 <= C::kStage, "a row tile's outputs fit a stage");
-  float* turn = reinterpret_cast<float*>(wave == 0 ? lds0 : wave == 1 ? lds1 : wave == 2 ? lds2 : lds3);
+  constexpr int kCols = TN * 32, kTurn = 32 * kCols * 4;
+  constexpr int kOnce = C::kStage * 4 / (NW * kTurn) < TM ? C::kStage * 4 / (NW * kTurn) : TM;  // row tiles turned at a time
+  constexpr int kShare = NW > 4 ? NW / 4 : 1;                                                    // waves that share a stage
+  static_assert(kOnce > 0 && TM % kOnce == 0 && NW % 4 == 0 && kOnce * kTurn * kShare <= C::kStage, "the waves' tiles fit the stages");
+  uint8_t* stage = wave < kShare ? lds0 : wave < 2 * kShare ? lds1 : wave < 3 * kShare ? lds2 : lds3;
+  float* turn = reinterpret_cast<float*>(stage + wave % kShare * kOnce * kTurn);
   const float* bias = a.bias ? a.bias + at.e * a.N : nullptr;
   const bool fours = by_fours(a);
+  constexpr int kWide = kCols / 4, kRows = 64 / kWide, R = 4;  // lanes along a row, rows at a time, those of a turn
+  const int c = lane % kWide * 4;
+  const int64_t n = n0 + c;
+  f32x4 b4{};
+  if (bias)
 #pragma unroll
-  for (int m = 0; m < TM; m++) {
+    for (int j = 0; j < 4; j++) b4[j] = n + j < a.N ? bias[n + j] : 0.0f;
 #pragma unroll
-    for (int t = 0; t < TN; t++)
+  for (int m0 = 0; m0 < TM; m0 += kOnce) {
 #pragma unroll
-      for (int r = 0; r < 16; r++) turn[(8 * (r >> 2) + 4 * h + (r & 3)) * kCols + t * 32 + i] = acc[t][m][r];
+    for (int m = 0; m < kOnce; m++)
+#pragma unroll
+      for (int t = 0; t < TN; t++)
+#pragma unroll
+        for (int r = 0; r < 16; r++) turn[(m * 32 + 8 * (r >> 2) + 4 * h + (r & 3)) * kCols + t * 32 + i] = acc[t][m0 + m][r];
     mx::wave_turn();
-    const int rows = at.rows - m * 32 < 32 ? at.rows - m * 32 : 32;
+    const int rows = at.rows - m0 * 32 < kOnce * 32 ? at.rows - m0 * 32 : kOnce * 32;
+    const int64_t y0 = at.m0 + m0 * 32;
     if (fours) {
 #pragma unroll 1
-      for (int o = lane; o < rows * (kCols / 4); o += 64) {
-        const int row = o / (kCols / 4), c = o % (kCols / 4) * 4;
-        const f32x4 z = *reinterpret_cast<const f32x4*>(turn + row * kCols + c);
-        const int64_t y = at.m0 + m * 32 + row, n = n0 + c;
-        if (n + 4 <= a.N)
-          finish4(a, bias, y, n, z);
-        else
+      for (int r0 = 0; r0 < rows; r0 += R * kRows) {
+        f32x4 z[R];
 #pragma unroll
-          for (int j = 0; j < 4; j++)
-            if (n + j < a.N) store_as(a.y, y * a.ys + n + j, finish(a, bias, y, n + j, z[j]), a.y_type);
+        for (int r = 0; r < R; r++) z[r] = *reinterpret_cast<const f32x4*>(turn + (r0 + r * kRows + lane / kWide) * kCols + c);
+        if (n + 4 <= a.N) {
+          finish4<R>(a, b4, y0 + r0 + lane / kWide, kRows, y0 + rows, n, z);
+        } else if (n < a.N) {
+#pragma unroll 1
+          for (int k = 0; k < R * 4; k++) {
+            const int row = r0 + (k >> 2) * kRows + lane / kWide;
+            if (row < rows && n + (k & 3) < a.N)
+              store_as(a.y, (y0 + row) * a.ys + n + (k & 3), finish(a, bias, y0 + row, n + (k & 3), turn[row * kCols + c + (k & 3)]), a.y_type);
+          }
+        }
       }
     } else {
 #pragma unroll 1
       for (int o = lane; o < rows * kCols; o += 64) {
-        const int64_t y = at.m0 + m * 32 + o / kCols, n = n0 + o % kCols;
-        if (n < a.N) store_as(a.y, y * a.ys + n, finish(a, bias, y, n, turn[o]), a.y_type);
+        const int64_t y = y0 + o / kCols, col = n0 + o % kCols;
+        if (col < a.N) store_as(a.y, y * a.ys + col, finish(a, bias, y, col, turn[o]), a.y_type);
       }
     }
     mx::wave_turn();
   }
 }
 
-template <int FMT, int XT, int TN, int TM, int OCC>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(OCC, OCC))) void k_linear_tiles(lin::Args a, int tiles_m, int tiles_n) {
+template <int FMT, int XT, int NW, int TN, int TM, int OCC>
+__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(OCC, OCC))) void k_linear_tiles(lin::Args a, int tiles_m, int tiles_n) {
   using namespace lin;
-  using C = LinTile<FMT, XT, TN, TM>;
+  using C = LinTile<FMT, XT, NW, TN, TM>;
   __shared__ __attribute__((aligned(16))) uint8_t lds0[C::kStage];
   __shared__ __attribute__((aligned(16))) uint8_t lds1[C::kStage];
   __shared__ __attribute__((aligned(16))) uint8_t lds2[C::kStage];
   __shared__ __attribute__((aligned(16))) uint8_t lds3[C::kStage];
-  __shared__ int64_t room[256 / 64 + 2];
-  RowTiles<256, C::kBM> groups(a, room);
+  __shared__ __attribute__((aligned(16))) uint8_t scales[NW * 2 * 1024];  // a wave's, twice
+  __shared__ int64_t room[NW + 2];
+  RowTiles<NW * 64, C::kBM> groups(a, room);
   int tm, tn;
   if (a.offsets) {  // an XCD (workgroups go round them) takes a run of items, along the weights of a row tile
     const int items = groups.all * tiles_n, xcd = blockIdx.x & 7, more = items & 7, nth = blockIdx.x >> 3;
@@ -269,22 +360,26 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(OCC, OCC)))
   }
   const RowTile at = groups.find(tm);
   if (at.rows <= 0) return;
-  lin_core<FMT, XT, TN, TM>(a, at, tn, lds0, lds1, lds2, lds3);
+  lin_core<FMT, XT, NW, TN, TM>(a, at, tn, lds0, lds1, lds2, lds3, scales);
 }
 
-template <int FMT, int XT, int TN, int TM, int OCC>
+template <int FMT, int XT, int NW, int TN, int TM, int OCC>
 int launch_tiles_as(const lin::Args& a, int64_t groups, hipStream_t s) {
-  using C = LinTile<FMT, XT, TN, TM>;
+  using C = LinTile<FMT, XT, NW, TN, TM>;
   const int64_t tm = a.offsets ? groups + a.R / C::kBM : (a.R + C::kBM - 1) / C::kBM, tn = (a.N + C::kBN - 1) / C::kBN;
   // with groups, up to seven workgroups more: the items are dealt to the XCDs in eight runs
   const int64_t grid = a.offsets ? (tm * tn + 7) / 8 * 8 : tm * tn;
   if (grid > kMaxGrid) return BQM_E_SHAPE;
-  hipLaunchKernelGGL((k_linear_tiles<FMT, XT, TN, TM, OCC>), dim3((unsigned)grid), dim3(256), 0, s, a, (int)tm, (int)tn);
+  hipLaunchKernelGGL((k_linear_tiles<FMT, XT, NW, TN, TM, OCC>), dim3((unsigned)grid), dim3(NW * 64), 0, s, a, (int)tm, (int)tn);
   return launch_status();
 }
 template <int FMT, int XT>
 int launch_tiles_of(const lin::Args& a, int64_t groups, hipStream_t s) {
-  return launch_tiles_as<FMT, XT, 2, XT == BQM_F32 ? 2 : 4, 2>(a, groups, s);
+#ifndef LT
+#define LT 4, 2, 4, 2
+#endif
+  if constexpr (XT == BQM_F32) return launch_tiles_as<FMT, XT, 4, 2, 2, 2>(a, groups, s);
+  else return launch_tiles_as<FMT, XT, LT>(a, groups, s);
 }
 
 }  // namespace
