@@ -41,6 +41,7 @@ constexpr uint32_t kOob = 0x80000000u;  // an offset past every descriptor: read
 __host__ __device__ constexpr int type_size(int type) { return type == BQM_F32 ? 4 : 2; }
 constexpr int parts_of(int type) { return type == BQM_F32 ? 3 : 1; }
 
+// The same value in every lane, as the compiler does not always see.
 __device__ __forceinline__ int64_t uniform(int64_t v) {
   return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32 | (uint32_t)__builtin_amdgcn_readfirstlane((int)v));
 }
@@ -65,11 +66,11 @@ __device__ __forceinline__ uint32_t f16_sixteenth(uint32_t v, float by) {
   return __builtin_bit_cast(uint32_t, r);
 }
 // Four codes of a word, one per byte (low nibbles to lo, high ones to hi), as pairs of 16-bit numbers.
-// Q4_0 comes out in units of kUnit.
+// Q4_0 comes out in units of kUnit, MXFP4 beside bf16 times `by`, a power of two.
 template <int FMT, int XT>
 constexpr float kUnit = FMT == BQM_Q4_0 && XT != BQM_F16 ? 0.0625f : 1.0f;
 template <int FMT, int XT>
-__device__ __forceinline__ void nibbles(uint32_t w, uint32_t (&lo)[2], uint32_t (&hi)[2]) {
+__device__ __forceinline__ void nibbles(uint32_t w, uint32_t (&lo)[2], uint32_t (&hi)[2], float by = 1.0f) {
   if constexpr (FMT == BQM_MXFP4) {  // the conversion takes the two nibbles of a byte
     const uint32_t w4 = w >> 4, l = (w & 0x000F000Fu) | (w4 & 0xFFF0FFF0u), h = (w4 & 0x000F000Fu) | ((w >> 8) & 0xFFF0FFF0u);
     if constexpr (XT == BQM_F16) {
@@ -78,10 +79,10 @@ __device__ __forceinline__ void nibbles(uint32_t w, uint32_t (&lo)[2], uint32_t 
       hi[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(h, 1.0f, 0));
       hi[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(h, 1.0f, 2));
     } else {
-      lo[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(l, 1.0f, 0));
-      lo[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(l, 1.0f, 2));
-      hi[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(h, 1.0f, 0));
-      hi[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(h, 1.0f, 2));
+      lo[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(l, by, 0));
+      lo[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(l, by, 2));
+      hi[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(h, by, 0));
+      hi[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(h, by, 2));
     }
   } else if constexpr (XT == BQM_F16) {
     const uint32_t b01 = __builtin_amdgcn_perm(0x64646464u, w, 0x04010400u), b23 = __builtin_amdgcn_perm(0x64646464u, w, 0x04030402u);
@@ -253,22 +254,34 @@ struct RowTile {
   int e, rows;   // group; rows of the tile, 0: no such tile
   int64_t m0;    // the first of them
 };
-// The row tiles of BM rows, groups ascending, as a workgroup of NT threads counts them (one barrier) and then
-// finds one of them (another).  Offsets are kept within the rows, so that whatever they hold, no row
-// outside is touched.  `room`: LDS, free again after the next barrier.
+// The row tiles of BM rows, as a workgroup of NT threads counts them (one barrier) and then finds one of them
+// (another): first the whole ones, groups ascending, then what is left of each group, so that the longest work
+// is given out first.  Offsets are kept within the rows, so that whatever they hold, no row outside is touched.
+// `room`: LDS, free again after the next barrier.
 template <int NT, int BM>
 struct RowTiles {
+  static constexpr int kWaves = NT / 64, kRoom = 2 * kWaves + 4;
   const Args& a;
-  int64_t (&room)[NT / 64 + 2];
-  int e0, e1, mine, before, all;
+  int (&room)[kRoom];
+  int e0, e1;              // the groups that this thread looks at
+  int whole, parts;        // tiles of the groups before these
+  int all_whole, all;
 
-  __device__ __forceinline__ int64_t at(int e) const {
-    const int64_t o = a.offsets[e];
-    return o < 0 ? (int64_t)0 : o < a.R ? o : a.R;
+  __device__ __forceinline__ int at(int e) const {
+    const int o = a.offsets[e];
+    return o < 0 ? 0 : o < a.R ? o : (int)a.R;
   }
-  __device__ __forceinline__ static int tiles_of(int64_t lo, int64_t hi) { return hi > lo ? (int)((hi - lo + BM - 1) / BM) : 0; }
+  template <typename F>
+  __device__ __forceinline__ void each(F&& f) const {  // f(group, first row, rows) for those that have any
+    int lo = e0 < e1 ? at(e0) : 0;
+    for (int e = e0; e < e1; e++) {
+      const int hi = at(e + 1);
+      if (hi > lo) f(e, lo, hi - lo);
+      lo = hi;
+    }
+  }
 
-  __device__ __forceinline__ RowTiles(const Args& args, int64_t (&lds)[NT / 64 + 2]) : a(args), room(lds) {
+  __device__ __forceinline__ RowTiles(const Args& args, int (&lds)[kRoom]) : a(args), room(lds) {
     if (!a.offsets) {
       all = (int)((a.R + BM - 1) / BM);
       return;
@@ -277,28 +290,23 @@ struct RowTiles {
     const int per = (a.E + NT - 1) / NT;
     e0 = tid * per < a.E ? tid * per : a.E;
     e1 = e0 + per < a.E ? e0 + per : a.E;
-    mine = 0;
-    int64_t lo = e0 < e1 ? at(e0) : 0;
-    for (int e = e0; e < e1; e++) {
-      const int64_t hi = at(e + 1);
-      mine += tiles_of(lo, hi);
-      lo = hi;
-    }
-    before = mine;
+    int w = 0, p = 0;
+    each([&](int, int, int rows) { w += rows / BM, p += rows % BM != 0; });
+    whole = w, parts = p;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
-      const int u = __shfl_up(before, o, 64);
-      if (lane >= o) before += u;
+      const int u = __shfl_up(whole, o, 64), v = __shfl_up(parts, o, 64);
+      if (lane >= o) whole += u, parts += v;
     }
-    if (lane == 63) room[wave] = before;
-    if (tid == 0) room[NT / 64] = -1;
+    if (lane == 63) room[wave] = whole, room[kWaves + wave] = parts;
+    if (tid == 0) room[2 * kWaves] = -1;
     __syncthreads();
-    before -= mine;
-    all = 0;
-    for (int k = 0; k < NT / 64; k++) {
-      const int n = __builtin_amdgcn_readfirstlane((int)room[k]);
-      if (k < wave) before += n;
-      all += n;
+    whole -= w, parts -= p;
+    all_whole = all = 0;
+    for (int k = 0; k < kWaves; k++) {
+      const int u = __builtin_amdgcn_readfirstlane(room[k]), v = __builtin_amdgcn_readfirstlane(room[kWaves + k]);
+      if (k < wave) whole += u, parts += v;
+      all_whole += u, all += u + v;
     }
   }
 
@@ -307,26 +315,21 @@ struct RowTiles {
       const int64_t m0 = (int64_t)tile * BM, left = a.R - m0;
       return {0, (int)(left < BM ? (left > 0 ? left : 0) : BM), m0};
     }
-    if (tile >= before && tile < before + mine) {
-      int first = before;
-      int64_t lo = at(e0);
-      for (int e = e0; e < e1; e++) {
-        const int64_t hi = at(e + 1);
-        const int k = tiles_of(lo, hi);
-        if (tile < first + k) {
-          room[NT / 64] = e;
-          room[NT / 64 + 1] = lo + (int64_t)(tile - first) * BM;
-          break;
-        }
-        first += k;
-        lo = hi;
+    int w = whole, p = all_whole + parts;
+    each([&](int e, int lo, int rows) {
+      const int n = rows / BM;
+      const bool first = tile >= w && tile < w + n, last = rows % BM != 0 && tile == p;
+      if (first || last) {
+        room[2 * kWaves] = e;
+        room[2 * kWaves + 1] = lo + (first ? tile - w : n) * BM;
+        room[2 * kWaves + 2] = first ? BM : rows % BM;
       }
-    }
+      w += n, p += rows % BM != 0;
+    });
     __syncthreads();
-    const int e = __builtin_amdgcn_readfirstlane((int)room[NT / 64]);
+    const int e = __builtin_amdgcn_readfirstlane(room[2 * kWaves]);
     if (e < 0) return {0, 0, 0};
-    const int64_t m0 = uniform(room[NT / 64 + 1]), left = uniform(at(e + 1)) - m0;
-    return {e, (int)(left < BM ? left : BM), m0};
+    return {e, __builtin_amdgcn_readfirstlane(room[2 * kWaves + 2]), (int64_t)__builtin_amdgcn_readfirstlane(room[2 * kWaves + 1])};
   }
 };
 

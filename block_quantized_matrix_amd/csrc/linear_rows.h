@@ -27,7 +27,7 @@ __global__ __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(OCC, OCC
   constexpr int CB = FMT == BQM_Q8_0 ? 32 : 16;         // code bytes of a block
   constexpr int L = FMT == BQM_Q8_0 ? 2 : 1;            // loads of a tile's step
   __shared__ __attribute__((aligned(16))) uint8_t lds[W * kWave];
-  __shared__ int64_t room[W + 2];
+  __shared__ int room[RowTiles<W * 64, RM>::kRoom];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i = lane & 15, q = lane >> 4;
   const int tile = blockIdx.x / span, run = blockIdx.x - tile * span;
@@ -291,8 +291,10 @@ int launch_linear(int fmt, const void* w, int E, const int32_t* offsets, int x_t
     a.scales_off = L.scales_off;
   }
   const int64_t groups = offsets ? (E < R ? E : R) : 1;
-  const int64_t each = (R + groups - 1) / groups;
-  return each > 64 ? launch_linear_tiles(fmt, x_type, a, groups, each, s) : launch_linear_rows(fmt, x_type, a, groups, each, s);
+#ifndef MOST
+#define MOST 16
+#endif
+  return R <= MOST ? launch_linear_rows(fmt, x_type, a, groups, (R + groups - 1) / groups, s) : launch_linear_tiles(fmt, x_type, a, groups, s);
 }
 
 }  // namespace bqm

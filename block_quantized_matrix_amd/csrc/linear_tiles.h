@@ -22,15 +22,18 @@ template <int FMT, int XT, int NW, int TN, int TM>
 struct LinTile {
   static constexpr int kWaves = NW, kBN = kWaves * TN * 32, kBM = TM * 32;
   static constexpr int kXB = lin::type_size(XT), kRow = 64 * kXB;  // bytes of a row's step
-  static constexpr int kStage = kBM * kRow, kPieces = kStage / (kWaves * 1024);
+  static constexpr int kStage = kBM * kRow, kRoom = kStage > NW * TN * 1024 ? kStage : NW * TN * 1024,  // LDS of a stage
+                        kPieces = (kStage / 1024 + kWaves - 1) / kWaves;
   static constexpr int kLoads = FMT == BQM_Q8_0 ? 2 : 1;           // of 16 bytes a lane, of a weight tile's step
   static_assert(TN <= 2, "a lane for each of a wave's rows");
-  static_assert(kStage % (kWaves * 1024) == 0, "whole loads");
+  static_assert(kStage % 1024 == 0, "whole loads");
 };
 
-template <int FMT, int XT, int NW, int TN, int TM>
-__device__ __forceinline__ void lin_core(const lin::Args& a, const lin::RowTile& at, int tn, uint8_t* lds0, uint8_t* lds1, uint8_t* lds2,
-                                         uint8_t* lds3, uint8_t* scales) {
+// The sums of a workgroup's tile.  FOLD (MXFP4 beside bf16): the block's scale goes into the codes' conversion,
+// exact for scales up to 2^125, and products add to the sums at once; else an FMA applies it to a block's sum.
+template <bool FOLD, int FMT, int XT, int NW, int TN, int TM>
+__device__ __forceinline__ void lin_sums(const lin::Args& a, const lin::RowTile& at, int tn, uint8_t* lds0, uint8_t* lds1, uint8_t* lds2,
+                                         uint8_t* lds3, uint8_t* scales, f32x16 (&acc)[TN][TM]) {
   using namespace lin;
   using C = LinTile<FMT, XT, NW, TN, TM>;
   constexpr int P = parts_of(XT), L = C::kLoads, PX = C::kPieces;
@@ -96,10 +99,12 @@ __device__ __forceinline__ void lin_core(const lin::Args& a, const lin::RowTile&
   const __amdgpu_buffer_rsrc_t rx = rsrc(a.x + at.m0 * a.xs, (int64_t)(at.rows - 1) * a.xs + (int64_t)nb * 32 * C::kXB);
   constexpr int kSlots = C::kRow / 16;  // 8, or 16 of fp32
   auto turned = [](int m) { return kSlots == 8 ? m >> 1 & 7 : m & 15; };
+  // where the waves do not divide the lots of 1024 bytes, some bring the last one too
+  auto lot_of = [&](int p) { return (p + 1) * NW <= C::kStage / 1024 || p * NW + wave < C::kStage / 1024 ? p * NW + wave : C::kStage / 1024 - 1; };
   uint32_t ox[PX];
 #pragma unroll
   for (int p = 0; p < PX; p++) {
-    const int u = (p * NW + wave) * 64 + lane, m = u / kSlots, slot = (u % kSlots ^ turned(m)) & (nb > 1 ? kSlots - 1 : kSlots / 2 - 1);
+    const int u = lot_of(p) * 64 + lane, m = u / kSlots, slot = (u % kSlots ^ turned(m)) & (nb > 1 ? kSlots - 1 : kSlots / 2 - 1);
     ox[p] = (uint32_t)((m < at.rows ? m : at.rows - 1) * (int)a.xs + slot * 16);
   }
   // The last step of an odd number of blocks takes the last two (of a single block: that block twice), so that
@@ -109,13 +114,12 @@ __device__ __forceinline__ void lin_core(const lin::Args& a, const lin::RowTile&
     const int at = 2 * s + 2 <= nb || nb == 1 ? 2 * s : nb - 2;
 #pragma unroll
     for (int p = 0; p < PX; p++)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (LdsPtr)(stage + (p * NW + wave) * 1024), 16, ox[p], at * (C::kRow / 2), 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (LdsPtr)(stage + lot_of(p) * 1024), 16, ox[p], at * (C::kRow / 2), 0, 0);
   };
   auto slot_at = [&](const uint8_t* stage, int t, int slot) {
     return *reinterpret_cast<const u32x4*>(stage + (t * 32 + i) * C::kRow + (slot ^ turned(i)) * 16);
   };
 
-  f32x16 acc[TN][TM] = {};
   auto meet = [&] {
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
@@ -143,12 +147,13 @@ __device__ __forceinline__ void lin_core(const lin::Args& a, const lin::RowTile&
         v = u32x4{v0, v1, v2, v3};
       }
       uint32_t lo[2][2], hi[2][2];
-      nibbles<FMT, XT>(v[2 * b], lo[0], hi[0]);
-      nibbles<FMT, XT>(v[2 * b + 1], lo[1], hi[1]);
+      const float by = FOLD ? __uint_as_float(scale << 23) : 1.0f;  // the conversion goes by the exponent field alone
+      nibbles<FMT, XT>(v[2 * b], lo[0], hi[0], by);
+      nibbles<FMT, XT>(v[2 * b + 1], lo[1], hi[1], by);
       w[0] = u32x4{lo[0][0], lo[0][1], lo[1][0], lo[1][1]};
       w[1] = u32x4{hi[0][0], hi[0][1], hi[1][0], hi[1][1]};
     }
-    f = scale_from<FMT, XT>(scale);
+    f = FOLD ? 1.0f : scale_from<FMT, XT>(scale);
     asm volatile("" : "+v"(w[0]), "+v"(w[1]), "+v"(f));  // here, not where the next block uses them
   };
   auto rows_of = [&](const uint8_t* stage, int m, int b, u32x4 (&x)[2][P]) {
@@ -169,8 +174,7 @@ __device__ __forceinline__ void lin_core(const lin::Args& a, const lin::RowTile&
       }
     }
   };
-  auto products = [&](const u32x4 (&x)[2][P], const u32x4 (&w)[2]) {
-    f32x16 sum{};
+  auto products = [&](const u32x4 (&x)[2][P], const u32x4 (&w)[2], f32x16 sum) {
 #pragma unroll
     for (int j = 0; j < 2; j++)
 #pragma unroll
@@ -191,7 +195,7 @@ __device__ __forceinline__ void lin_core(const lin::Args& a, const lin::RowTile&
   constexpr int K = TM * TN;
   u32x4 w[TN][2], x[2][P];
   float f[TN], f_last;
-  f32x16 sum[2];
+  f32x16 sum[2];  // in turn, from block 0 to block 1 too
   auto block = [&](auto bc, int s, int next_d, const uint8_t* stage, const uint8_t* next_stage, auto&& between) {
     constexpr int B = decltype(bc)::value;
     float g[TN];
@@ -199,23 +203,28 @@ __device__ __forceinline__ void lin_core(const lin::Args& a, const lin::RowTile&
 #pragma unroll
     for (int k = 0; k < K; k++) {
       const int m = k / TN, t = k % TN;
-      if (k == K / 2) between();
-      sum[k & 1] = products(x, w[t]);
+      if (k == (K - 1) / 2) between();
+      if constexpr (FOLD)
+        acc[t][m] = products(x, w[t], acc[t][m]);
+      else
+        sum[(k + B * K) & 1] = products(x, w[t], f32x16{});
       if (t == TN - 1) {
         if (m + 1 < TM)
           rows_of(stage, m + 1, B, x);
         else
           rows_of(next_stage, 0, B ^ 1, x);
       }
-      if (k > 0)
-        add_scaled(acc[(k - 1) % TN][(k - 1) / TN], sum[(k - 1) & 1], f[(k - 1) % TN]);
-      else if (B == 1)
-        add_scaled(acc[TN - 1][TM - 1], sum[(K - 1) & 1], f_last);
-      if (m == TM - 2) bits[t] = scale_at(t, B ? s + 1 : s, B ^ 1);
+      if constexpr (!FOLD) {
+        if (k > 0)
+          add_scaled(acc[(k - 1) % TN][(k - 1) / TN], sum[(k - 1 + B * K) & 1], f[(k - 1) % TN]);
+        else if (B == 1)
+          add_scaled(acc[TN - 1][TM - 1], sum[(K - 1) & 1], f_last);
+      }
+      if (m == (TM > 1 ? TM - 2 : 0)) bits[t] = scale_at(t, B ? s + 1 : s, B ^ 1);
       if (m == TM - 1) convert(B ^ 1, next_d, t, bits[t], w[t], g[t]);
       __builtin_amdgcn_sched_barrier(0);
     }
-    if (B == 1) add_scaled(acc[TN - 1][TM - 1], sum[(K - 1) & 1], f[TN - 1]);
+    if (B == 1 && !FOLD) add_scaled(acc[TN - 1][TM - 1], sum[(K - 1 + B * K) & 1], f[TN - 1]);
     f_last = f[TN - 1];
 #pragma unroll
     for (int t = 0; t < TN; t++) f[t] = g[t];
@@ -260,33 +269,70 @@ __device__ __forceinline__ void lin_core(const lin::Args& a, const lin::RowTile&
     for (int t = 0; t < TN; t++) convert(0, 0, t, scale_at(t, 0, 0), w[t], f[t]);
     if constexpr (L == 2) load_codes(0, 2);
     __builtin_amdgcn_sched_barrier(0);
-    for (int s = 0; s < whole; s += 4) {
+    int s = 0;  // (left in one place only: exits from each step had the sums copied, and spilled)
+    for (; s + 4 <= whole; s += 4) {
       step(std::integral_constant<int, 0>{}, s, lds0, lds1, lds3);
-      if (s + 1 >= whole) break;
       step(std::integral_constant<int, 1>{}, s + 1, lds1, lds2, lds0);
-      if (s + 2 >= whole) break;
       step(std::integral_constant<int, 2>{}, s + 2, lds2, lds3, lds1);
-      if (s + 3 >= whole) break;
       step(std::integral_constant<int, 3>{}, s + 3, lds3, lds0, lds2);
     }
+    if (s < whole) step(std::integral_constant<int, 0>{}, s, lds0, lds1, lds3);
+    if (s + 1 < whole) step(std::integral_constant<int, 1>{}, s + 1, lds1, lds2, lds0);
+    if (s + 2 < whole) step(std::integral_constant<int, 2>{}, s + 2, lds2, lds3, lds1);
     if (nb & 1) {  // a last block without a partner, its codes already at hand
       const uint8_t* stage = (whole & 3) == 0 ? lds0 : (whole & 3) == 1 ? lds1 : (whole & 3) == 2 ? lds2 : lds3;
 #pragma unroll
       for (int m = 0; m < TM; m++) {
         rows_of(stage, m, nb > 1, x);
 #pragma unroll
-        for (int t = 0; t < TN; t++) add_scaled(acc[t][m], products(x, w[t]), f[t]);
+        for (int t = 0; t < TN; t++) {
+          if constexpr (FOLD)
+            acc[t][m] = products(x, w[t], acc[t][m]);
+          else
+            add_scaled(acc[t][m], products(x, w[t], f32x16{}), f[t]);
+        }
       }
     }
   }
   vm_wait<0>();  // nothing may be on its way into LDS when it is used again
   __syncthreads();
+}
+
+template <int FMT, int XT, int NW, int TN, int TM>
+__device__ __forceinline__ void lin_core(const lin::Args& a, const lin::RowTile& at, int tn, uint8_t* lds0, uint8_t* lds1, uint8_t* lds2,
+                                         uint8_t* lds3, uint8_t* scales) {
+  using namespace lin;
+  using C = LinTile<FMT, XT, NW, TN, TM>;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int i = lane & 31, h = lane >> 5;
+  const int64_t n0 = (int64_t)tn * C::kBN + wave * TN * 32;
+  constexpr bool FOLD = FMT == BQM_MXFP4 && XT != BQM_F16;
+  f32x16 acc[TN][TM] = {};
+  lin_sums<FOLD, FMT, XT, NW, TN, TM>(a, at, tn, lds0, lds1, lds2, lds3, scales, acc);
+  if constexpr (FOLD) {
+    // Scales beyond 2^125, whose largest weights bf16 does not hold, and the scale NaN leave sums that are not
+    // numbers, as such inputs do: these tiles are made again with the scales apart.
+    float probe = 0;
+#pragma unroll
+    for (int t = 0; t < TN; t++)
+#pragma unroll
+      for (int m = 0; m < TM; m++)
+#pragma unroll
+        for (int r = 0; r < 16; r++) probe = fmaf(acc[t][m][r], 0.0f, probe);  // NaN if any is not finite
+    if (__builtin_expect(__syncthreads_or(probe != probe), 0)) {
+#pragma unroll
+      for (int t = 0; t < TN; t++)
+#pragma unroll
+        for (int m = 0; m < TM; m++) acc[t][m] = f32x16{};
+      lin_sums<false, FMT, XT, NW, TN, TM>(a, at, tn, lds0, lds1, lds2, lds3, scales, acc);
+    }
+  }
   // A lane holds column i of a weight tile, rows 8 (r / 4) + 4 h + r % 4 of a row tile.  Each wave turns its row
   // tiles in a stage of its own, so that it stores whole runs of a row of Y.
   constexpr int kCols = TN * 32, kTurn = 32 * kCols * 4;
-  constexpr int kOnce = C::kStage * 4 / (NW * kTurn) < TM ? C::kStage * 4 / (NW * kTurn) : TM;  // row tiles turned at a time
-  constexpr int kShare = NW > 4 ? NW / 4 : 1;                                                    // waves that share a stage
-  static_assert(kOnce > 0 && TM % kOnce == 0 && NW % 4 == 0 && kOnce * kTurn * kShare <= C::kStage, "the waves' tiles fit the stages");
+  constexpr int kRoom = C::kRoom / (((NW + 3) / 4) * kTurn), kOnce = kRoom >= TM ? TM : kRoom >= TM / 2 && TM % 2 == 0 ? TM / 2 : 1;  // row tiles turned at a time
+  constexpr int kShare = (NW + 3) / 4;  // waves that share a stage
+  static_assert(kOnce > 0 && TM % kOnce == 0 && kOnce * kTurn * kShare <= C::kRoom, "the waves' tiles fit the stages");
   uint8_t* stage = wave < kShare ? lds0 : wave < 2 * kShare ? lds1 : wave < 3 * kShare ? lds2 : lds3;
   float* turn = reinterpret_cast<float*>(stage + wave % kShare * kOnce * kTurn);
   const float* bias = a.bias ? a.bias + at.e * a.N : nullptr;
@@ -341,55 +387,101 @@ template <int FMT, int XT, int NW, int TN, int TM, int OCC>
 __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(OCC, OCC))) void k_linear_tiles(lin::Args a, int tiles_m, int tiles_n) {
   using namespace lin;
   using C = LinTile<FMT, XT, NW, TN, TM>;
-  __shared__ __attribute__((aligned(16))) uint8_t lds0[C::kStage];
-  __shared__ __attribute__((aligned(16))) uint8_t lds1[C::kStage];
-  __shared__ __attribute__((aligned(16))) uint8_t lds2[C::kStage];
-  __shared__ __attribute__((aligned(16))) uint8_t lds3[C::kStage];
+  __shared__ __attribute__((aligned(16))) uint8_t lds0[C::kRoom];
+  __shared__ __attribute__((aligned(16))) uint8_t lds1[C::kRoom];
+  __shared__ __attribute__((aligned(16))) uint8_t lds2[C::kRoom];
+  __shared__ __attribute__((aligned(16))) uint8_t lds3[C::kRoom];
   __shared__ __attribute__((aligned(16))) uint8_t scales[NW * 2 * 1024];  // a wave's, twice
-  __shared__ int64_t room[NW + 2];
+  __shared__ int room[RowTiles<NW * 64, C::kBM>::kRoom];
   RowTiles<NW * 64, C::kBM> groups(a, room);
   int tm, tn;
-  if (a.offsets) {  // an XCD (workgroups go round them) takes a run of items, along the weights of a row tile
-    const int items = groups.all * tiles_n, xcd = blockIdx.x & 7, more = items & 7, nth = blockIdx.x >> 3;
-    if (nth >= (items >> 3) + (xcd < more)) return;  // none left, the whole workgroup
-    const int item = xcd * (items >> 3) + (xcd < more ? xcd : more) + nth;
-    tm = item / tiles_n, tn = item - tm * tiles_n;
+  if (a.offsets) {  // row tiles go round the XCDs (as workgroups do), each with all its columns: its rows come to one L2 only
+    const int nth = blockIdx.x >> 3, turn = nth / tiles_n;
+    tm = turn * 8 + (blockIdx.x & 7), tn = nth - turn * tiles_n;
+    if (tm >= groups.all) return;  // the whole workgroup
   } else {
     const MxPlace at = mx_place(blockIdx.x, tiles_m, tiles_n);
     tm = at.m, tn = at.n;
   }
   const RowTile at = groups.find(tm);
   if (at.rows <= 0) return;
-  lin_core<FMT, XT, NW, TN, TM>(a, at, tn, lds0, lds1, lds2, lds3, scales);
+  // a tile of few rows (the last of a group) as one of a lower height
+  if (TM > 1 && at.rows <= 32)
+    lin_core<FMT, XT, NW, TN, 1>(a, at, tn, lds0, lds1, lds2, lds3, scales);
+  else if (TM > 2 && at.rows <= 64)
+    lin_core<FMT, XT, NW, TN, 2>(a, at, tn, lds0, lds1, lds2, lds3, scales);
+  else
+    lin_core<FMT, XT, NW, TN, TM>(a, at, tn, lds0, lds1, lds2, lds3, scales);
 }
 
 template <int FMT, int XT, int NW, int TN, int TM, int OCC>
 int launch_tiles_as(const lin::Args& a, int64_t groups, hipStream_t s) {
   using C = LinTile<FMT, XT, NW, TN, TM>;
   const int64_t tm = a.offsets ? groups + a.R / C::kBM : (a.R + C::kBM - 1) / C::kBM, tn = (a.N + C::kBN - 1) / C::kBN;
-  // with groups, up to seven workgroups more: the items are dealt to the XCDs in eight runs
-  const int64_t grid = a.offsets ? (tm * tn + 7) / 8 * 8 : tm * tn;
+  const int64_t grid = (a.offsets ? (tm + 7) / 8 * 8 : tm) * tn;
   if (grid > kMaxGrid) return BQM_E_SHAPE;
   hipLaunchKernelGGL((k_linear_tiles<FMT, XT, NW, TN, TM, OCC>), dim3((unsigned)grid), dim3(NW * 64), 0, s, a, (int)tm, (int)tn);
   return launch_status();
 }
+// The tiles, and their step's time (us; 64 of K) where a unit holds one to `resident` workgroups.
+struct LinChoice {
+  int tn, tm, resident;
+  float step[4];
+};
+// Measured with Q4_0 and bf16 rows, N = 17408 and 4096 and K = 5120 and 4096.
+constexpr LinChoice kLinChoices[] = {{1, 1, 4, {0.46f, 0.61f, 0.80f, 1.15f}},
+                                     {1, 2, 3, {0.58f, 0.79f, 1.10f}},
+                                     {1, 3, 2, {0.68f, 0.95f}},
+                                     {1, 4, 2, {0.82f, 1.19f}},
+                                     {2, 4, 2, {1.50f, 2.05f}}};
+constexpr LinChoice kLinChoices32[] = {{1, 1, 3, {0.60f, 0.90f, 1.30f}}, {1, 2, 2, {0.9f, 1.4f}}, {2, 2, 2, {1.4f, 2.4f}}};
+
 template <int FMT, int XT>
-int launch_tiles_of(const lin::Args& a, int64_t groups, hipStream_t s) {
-#ifndef LT
-#define LT 4, 2, 4, 2
-#endif
-  if constexpr (XT == BQM_F32) return launch_tiles_as<FMT, XT, 4, 2, 2, 2>(a, groups, s);
-  else return launch_tiles_as<FMT, XT, LT>(a, groups, s);
+int launch_tiles_of(const lin::Args& a, int64_t groups, int choice, hipStream_t s) {
+  if constexpr (XT == BQM_F32)
+    return choice == 0 ? launch_tiles_as<FMT, XT, 4, 1, 1, 3>(a, groups, s)
+           : choice == 1 ? launch_tiles_as<FMT, XT, 4, 1, 2, 2>(a, groups, s)
+                         : launch_tiles_as<FMT, XT, 4, 2, 2, 2>(a, groups, s);
+  else
+    return choice == 0 ? launch_tiles_as<FMT, XT, 4, 1, 1, 4>(a, groups, s)
+           : choice == 1 ? launch_tiles_as<FMT, XT, 4, 1, 2, 3>(a, groups, s)
+           : choice == 2 ? launch_tiles_as<FMT, XT, 4, 1, 3, 2>(a, groups, s)
+           : choice == 3 ? launch_tiles_as<FMT, XT, 4, 1, 4, 2>(a, groups, s)
+                         : launch_tiles_as<FMT, XT, 4, 2, 4, 2>(a, groups, s);
 }
 
 }  // namespace
 
-int launch_linear_tiles(int fmt, int x_type, const lin::Args& a, int64_t groups, int64_t rows_each, hipStream_t s) {
-  (void)rows_each;
-#define BQM_TILES(FMT)                                                   \
-  return x_type == BQM_F32   ? launch_tiles_of<FMT, BQM_F32>(a, groups, s) \
-         : x_type == BQM_F16 ? launch_tiles_of<FMT, BQM_F16>(a, groups, s) \
-                             : launch_tiles_of<FMT, BQM_BF16>(a, groups, s)
+// The index of the tile.  One matrix: the least time by the table, rounds of workgroups on 256 units.  Groups,
+// of whose lengths the host knows only the mean: by that.  (The tests ask too: they have to run every tile.)
+extern "C" int bqm_internal_linear_choice(int x_type, int grouped, int64_t R, int64_t N, int64_t K, int64_t groups) {
+  const LinChoice* table = x_type == BQM_F32 ? kLinChoices32 : kLinChoices;
+  const int count = x_type == BQM_F32 ? 3 : 5;
+  if (grouped) {
+    const int64_t mean = R / (groups > 0 ? groups : 1);
+    if (x_type == BQM_F32) return mean <= 16 ? 0 : (groups + R / 64) * ((N + 255) / 256) < 512 ? 1 : 2;
+    const int c = mean <= 6 ? 0 : mean <= 20 ? 1 : mean <= 96 ? 2 : 4;
+    return c == 4 && (groups + R / 128) * ((N + 255) / 256) < 512 ? 3 : c;
+  }
+  int best = 0;
+  double least = 0;
+  for (int c = 0; c < count; c++) {
+    const LinChoice& t = table[c];
+    const int64_t wgs = ((R + t.tm * 32 - 1) / (t.tm * 32)) * ((N + t.tn * 128 - 1) / (t.tn * 128)), round = 256 * t.resident;
+    const int64_t full = wgs / round, left = wgs % round;
+    const double step = full * t.step[t.resident - 1] + (left ? t.step[(left - 1) / 256] : 0.0f);
+    const double time = (double)((K + 63) / 64) * step + 4.0 * (full + (left > 0));
+    if (c == 0 || time < least) best = c, least = time;
+  }
+  return best;
+}
+
+int launch_linear_tiles(int fmt, int x_type, const lin::Args& a, int64_t groups, hipStream_t s) {
+  const int c = bqm_internal_linear_choice(x_type, a.offsets != nullptr, a.R, a.N, (int64_t)a.nb * kQK, groups);
+#define BQM_TILES(FMT)                                                      \
+  return x_type == BQM_F32   ? launch_tiles_of<FMT, BQM_F32>(a, groups, c, s) \
+         : x_type == BQM_F16 ? launch_tiles_of<FMT, BQM_F16>(a, groups, c, s) \
+                             : launch_tiles_of<FMT, BQM_BF16>(a, groups, c, s)
   if (fmt == BQM_Q4_0) BQM_TILES(BQM_Q4_0);
   if (fmt == BQM_Q8_0) BQM_TILES(BQM_Q8_0);
   BQM_TILES(BQM_MXFP4);
