@@ -156,6 +156,12 @@ __device__ __forceinline__ void store_as(uint8_t* p, int64_t at, float v, int ty
     reinterpret_cast<uint16_t*>(p)[at] = bits16(v, type);
 }
 
+// z / (1 + 2^u).  The exponential and the reciprocal are the hardware's, each off by a step of fp32 at most, and
+// u's rounding counts |u| 2^-24 of the exponential: no more than a step of z where that counts.  (With expf and a
+// correctly rounded division the 512-token product of 17408 x 5120 takes 12 us longer.)
+__device__ __forceinline__ float over_one_plus_exp2(float z, float u) {
+  return z * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(u));
+}
 // The two gelus are written with the tail of their distribution, which keeps its digits far below 0.
 template <int V>
 __device__ __forceinline__ void activate(float (&z)[V], int act) {
@@ -164,13 +170,13 @@ __device__ __forceinline__ void activate(float (&z)[V], int act) {
     for (int j = 0; j < V; j++) z[j] = z[j] < 0.0f ? 0.0f : z[j];  // a NaN stays
   } else if (act == BQM_ACT_SILU) {
 #pragma unroll
-    for (int j = 0; j < V; j++) z[j] = z[j] / (1.0f + expf(-z[j]));
+    for (int j = 0; j < V; j++) z[j] = over_one_plus_exp2(z[j], z[j] * -1.44269504f);
   } else if (act == BQM_ACT_GELU) {
 #pragma unroll
     for (int j = 0; j < V; j++) z[j] = 0.5f * z[j] * erfcf(z[j] * -0.70710678f);
   } else if (act == BQM_ACT_GELU_TANH) {
 #pragma unroll
-    for (int j = 0; j < V; j++) z[j] = z[j] / (1.0f + expf(-1.5957691f * (z[j] + 0.044715f * z[j] * z[j] * z[j])));
+    for (int j = 0; j < V; j++) z[j] = over_one_plus_exp2(z[j], -2.30220819f * (z[j] + 0.044715f * z[j] * z[j] * z[j]));
   }
 }
 // y of row m (of all rows) and column n, whose group's bias starts at `bias`.

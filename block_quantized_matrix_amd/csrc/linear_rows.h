@@ -154,6 +154,7 @@ __global__ __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(OCC, OCC
           for (int p = 0; p < P; p++) xop[u][tm][p] = operand(u, tm, p);
 #pragma unroll
       for (int t = 0; t < T; t++) {
+        if (t * 16 < (int)(r1 - r0)) {  // (loads go on: a branch around them would make the compiler wait for all)
         // words (or pairs of them) of the four blocks to the lane groups, and each block's scale to all
         uint32_t wop[4][4];
 #pragma unroll
@@ -182,6 +183,7 @@ __global__ __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(OCC, OCC
         mma::exchange<true>(fs);
 #pragma unroll
         for (int tm = 0; tm < TM; tm++)
+          if (TM == 1 || tm * 16 < at.rows)
 #pragma unroll
           for (int u = 0; u < 4; u++) {
             const u32x4 w{wop[u][0], wop[u][1], wop[u][2], wop[u][3]};
@@ -197,6 +199,7 @@ __global__ __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(OCC, OCC
 #pragma unroll
             for (int r = 0; r < 4; r++) acc[t][tm][r] = fmaf(__uint_as_float(fs[u]), sum[r], acc[t][tm][r]);
           }
+        }
         __builtin_amdgcn_sched_barrier(0);
         load_w(d, t, s + D * W);
       }
@@ -231,7 +234,7 @@ struct RowsPlan {
 
 template <int FMT, int XT, int RM, int T>
 int launch_rows_as(const lin::Args& a, const RowsPlan& p, hipStream_t s) {
-  constexpr int W = T <= 2 && RM <= 16 && (XT != BQM_F32 || RM < 16) ? 16 : 8;
+  constexpr int W = (XT != BQM_F32 && RM <= 16 && T <= 3) || (RM <= 4 && T <= 2) ? 16 : 8;
   constexpr int D = T == 1 ? 2 : 1;
   hipLaunchKernelGGL((k_linear_rows<FMT, XT, RM, T, D, W, W / 4>), dim3((unsigned)(p.tiles * p.span)), dim3(W * 64), 0, s, a, p.halves,
                      (int)p.span);
@@ -243,11 +246,12 @@ int launch_rows_of(const lin::Args& a, const RowsPlan& p, hipStream_t s) {
 #define BQM_ROWS(RM)                                         \
   return T <= 1   ? launch_rows_as<FMT, XT, RM, 1>(a, p, s)  \
          : T <= 2 ? launch_rows_as<FMT, XT, RM, 2>(a, p, s)  \
-         : T <= 4 ? launch_rows_as<FMT, XT, RM, 4>(a, p, s)  \
+         : T <= 3 ? launch_rows_as<FMT, XT, RM, 3>(a, p, s)  \
+         : T <= 5 ? launch_rows_as<FMT, XT, RM, 5>(a, p, s)  \
                   : launch_rows_as<FMT, XT, RM, 9>(a, p, s)
   if (p.rm == 4) BQM_ROWS(4);
   if constexpr (XT != BQM_F32)
-    if (p.rm == 64) return T <= 2 ? launch_rows_as<FMT, XT, 64, 2>(a, p, s) : launch_rows_as<FMT, XT, 64, 4>(a, p, s);
+    if (p.rm == 64) return launch_rows_as<FMT, XT, 64, 2>(a, p, s);
   BQM_ROWS(16);
 #undef BQM_ROWS
 }
@@ -259,7 +263,7 @@ int launch_linear_rows(int fmt, int x_type, const lin::Args& a, int64_t groups, 
   p.rm = rows_each <= 4 ? 4 : rows_each <= 16 || x_type == BQM_F32 ? 16 : 64;
   // exactly, or a partial tile per group at most, plus the full ones
   p.tiles = a.offsets ? groups + a.R / p.rm : (a.R + p.rm - 1) / p.rm;
-  const int64_t runs = (a.N + 7) / 8, most = p.rm == 64 ? 8 : 18;
+  const int64_t runs = (a.N + 7) / 8, most = p.rm == 64 ? 4 : 18;
   const int64_t rounds = (runs * p.tiles + 256 * most - 1) / (256 * most);
   p.halves = (int)((runs * p.tiles + 256 * rounds - 1) / (256 * rounds));
   p.halves = p.halves > most ? (int)most : p.halves < runs ? p.halves : (int)runs;
@@ -275,7 +279,17 @@ int launch_linear_rows(int fmt, int x_type, const lin::Args& a, int64_t groups, 
 #undef BQM_ROWS
 }
 
-// Rows of an expert if all were used alike: what the tile goes by.
+// Which of the two kernels: 1 for the one above.  Up to 16 rows it wins everywhere (17408 x 5120, Q4_0: 16 rows
+// 21.5 us, by tiles 40; 32 rows 63 and 40).  With more it does where its workgroups, which share K out among
+// their waves, are one round on 256 units (1024 x 4096: 512 rows 16 us, by tiles 29, 1024 rows 48 and 29;
+// 5120 x 17408, 64 rows 58 and 165); fp32 rows, of which it takes 16 at a time, up to four (4096 x 4096: 64 rows
+// 19 and 59, 256 rows 55 and 64).
+extern "C" int bqm_internal_linear_rows(int x_type, int grouped, int64_t R, int64_t N, int64_t groups) {
+  if (R <= 16) return 1;
+  const int64_t each = x_type == BQM_F32 ? 16 : 64;
+  return (grouped ? groups + R / each : (R + each - 1) / each) * ((N + 31) / 32) <= (x_type == BQM_F32 ? 1024 : 256);
+}
+
 int launch_linear(int fmt, const void* w, int E, const int32_t* offsets, int x_type, const void* X, int64_t x_stride,
                   const float* bias, int act, const void* mul, int64_t mul_stride, const void* res, int64_t res_stride,
                   int y_type, void* Y, int64_t y_stride, int64_t R, int64_t N, int64_t K, hipStream_t s) {
@@ -291,10 +305,9 @@ int launch_linear(int fmt, const void* w, int E, const int32_t* offsets, int x_t
     a.scales_off = L.scales_off;
   }
   const int64_t groups = offsets ? (E < R ? E : R) : 1;
-#ifndef MOST
-#define MOST 16
-#endif
-  return R <= MOST ? launch_linear_rows(fmt, x_type, a, groups, (R + groups - 1) / groups, s) : launch_linear_tiles(fmt, x_type, a, groups, s);
+  if (bqm_internal_linear_rows(x_type, offsets != nullptr, R, N, groups))
+    return launch_linear_rows(fmt, x_type, a, groups, (R + groups - 1) / groups, s);
+  return launch_linear_tiles(fmt, x_type, a, groups, s);
 }
 
 }  // namespace bqm

@@ -90,7 +90,8 @@ __device__ __forceinline__ void lin_sums(const lin::Args& a, const lin::RowTile&
   auto keep_scales = [&](int g) { *reinterpret_cast<u32x4*>(sc + (g & 1) * 1024 + lane * 16) = fresh; };
   auto scale_at = [&](int t, int s, int b) {  // of block b of step s
     const uint8_t* p = sc + (s >> 2 & 1) * 1024 + (t * 32 + i) * 16;
-    if constexpr (MX) return (uint32_t)p[((s & 1) * 2 + b) * 4 + (s >> 1 & 3)];
+    // (as a word: what is read as bytes might be any LDS to the compiler, which then waits for the loads into it)
+    if constexpr (MX) return reinterpret_cast<const uint32_t*>(p)[(s & 1) * 2 + b] >> (8 * (s >> 1 & 3)) & 0xFF;
     return (uint32_t)reinterpret_cast<const uint16_t*>(p)[(s & 3) * 2 + b];
   };
 
@@ -233,6 +234,10 @@ __device__ __forceinline__ void lin_sums(const lin::Args& a, const lin::RowTile&
   auto step = [&](auto qc, int s, const uint8_t* cur, const uint8_t* nxt, uint8_t* free) {
     constexpr int Q = decltype(qc)::value, d = Q & 1;
     // codes: block 0 converts block 1 of this step, block 1 block 0 of the next
+    if constexpr (L == 2) {
+      load_codes(0, 2 * s + 2);
+      __builtin_amdgcn_sched_barrier(0);
+    }
     block(std::integral_constant<int, 0>{}, s, L == 2 ? 1 : d, cur, cur, [] {});
     load_codes(L == 2 ? 1 : d, L == 2 ? 2 * s + 3 : s + 2);
     if constexpr (Q == 0) load_scales((s >> 2) + 1);
@@ -240,15 +245,15 @@ __device__ __forceinline__ void lin_sums(const lin::Args& a, const lin::RowTile&
       keep_scales((s >> 2) + 1);
       mx::wave_turn();
     }
-    if constexpr (L == 1) __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_sched_barrier(0);
     block(std::integral_constant<int, 1>{}, s, L == 2 ? 0 : d ^ 1, cur, nxt, [&] {
-      // the rows of step s + 1 have arrived, and every wave has read all of step s - 1
-      vm_wait<PX + TN>();
+      // The rows of step s + 1 have arrived (after them came those of step s + 2, the codes of two blocks of
+      // nibbles or four of bytes, and the scales of every fourth step), and every wave has read all of step s - 1.
+      vm_wait<PX + (L == 2 ? 4 : 2) * TN + (Q <= 1 ? (MX ? 4 : 1) : 0)>();
       meet();
       load_x(s + 3, free);
       __builtin_amdgcn_sched_barrier(0);
     });
-    if constexpr (L == 2) load_codes(0, 2 * s + 4);
     __builtin_amdgcn_sched_barrier(0);
   };
   const int whole = nb >> 1;
@@ -267,7 +272,6 @@ __device__ __forceinline__ void lin_sums(const lin::Args& a, const lin::RowTile&
     rows_of(lds0, 0, 0, x);
 #pragma unroll
     for (int t = 0; t < TN; t++) convert(0, 0, t, scale_at(t, 0, 0), w[t], f[t]);
-    if constexpr (L == 2) load_codes(0, 2);
     __builtin_amdgcn_sched_barrier(0);
     int s = 0;  // (left in one place only: exits from each step had the sums copied, and spilled)
     for (; s + 4 <= whole; s += 4) {
@@ -423,25 +427,26 @@ int launch_tiles_as(const lin::Args& a, int64_t groups, hipStream_t s) {
   hipLaunchKernelGGL((k_linear_tiles<FMT, XT, NW, TN, TM, OCC>), dim3((unsigned)grid), dim3(NW * 64), 0, s, a, (int)tm, (int)tn);
   return launch_status();
 }
-// The tiles, and their step's time (us; 64 of K) where a unit holds one to `resident` workgroups.
+// The tiles: weight tiles and row tiles of 32 a wave, workgroups that a unit holds at most, and the time of a
+// step (us; 64 of K) where it holds one, two, ... of them, measured with N = 17408 and K = 5120, weights from
+// memory.  (fp32 rows take four times the LDS of the others' step, so their tiles are lower.)
 struct LinChoice {
   int tn, tm, resident;
   float step[4];
 };
-// Measured with Q4_0 and bf16 rows, N = 17408 and 4096 and K = 5120 and 4096.
-constexpr LinChoice kLinChoices[] = {{1, 1, 4, {0.46f, 0.61f, 0.80f, 1.15f}},
-                                     {1, 2, 3, {0.58f, 0.79f, 1.10f}},
-                                     {1, 3, 2, {0.68f, 0.95f}},
-                                     {1, 4, 2, {0.82f, 1.19f}},
-                                     {2, 4, 2, {1.50f, 2.05f}}};
-constexpr LinChoice kLinChoices32[] = {{1, 1, 3, {0.60f, 0.90f, 1.30f}}, {1, 2, 2, {0.9f, 1.4f}}, {2, 2, 2, {1.4f, 2.4f}}};
+constexpr int kLinTiles = 5, kLinTiles32 = 2;
+constexpr LinChoice kLinQ4[kLinTiles] = {{1, 1, 4, {0.46f, 0.61f, 0.85f, 0.95f}}, {1, 2, 3, {0.58f, 0.80f, 1.08f}}, {1, 3, 2, {0.68f, 0.95f}},
+                                         {1, 4, 2, {0.81f, 1.17f}}, {2, 4, 2, {1.45f, 2.05f}}};
+constexpr LinChoice kLinQ8[kLinTiles] = {{1, 1, 4, {0.68f, 0.98f, 1.28f, 1.32f}}, {1, 2, 3, {0.75f, 1.08f, 1.47f}}, {1, 3, 2, {0.80f, 1.10f}},
+                                         {1, 4, 2, {0.87f, 1.36f}}, {2, 4, 2, {1.53f, 2.15f}}};
+constexpr LinChoice kLinMx[kLinTiles] = {{1, 1, 4, {0.38f, 0.43f, 0.55f, 0.60f}}, {1, 2, 3, {0.42f, 0.54f, 0.76f}}, {1, 3, 2, {0.50f, 0.67f}},
+                                         {1, 4, 2, {0.57f, 0.83f}}, {2, 4, 2, {0.93f, 1.37f}}};
+constexpr LinChoice kLin32[kLinTiles32] = {{1, 1, 3, {0.92f, 1.35f, 1.85f}}, {2, 2, 2, {2.03f, 2.90f}}};
 
 template <int FMT, int XT>
 int launch_tiles_of(const lin::Args& a, int64_t groups, int choice, hipStream_t s) {
   if constexpr (XT == BQM_F32)
-    return choice == 0 ? launch_tiles_as<FMT, XT, 4, 1, 1, 3>(a, groups, s)
-           : choice == 1 ? launch_tiles_as<FMT, XT, 4, 1, 2, 2>(a, groups, s)
-                         : launch_tiles_as<FMT, XT, 4, 2, 2, 2>(a, groups, s);
+    return choice == 0 ? launch_tiles_as<FMT, XT, 4, 1, 1, 3>(a, groups, s) : launch_tiles_as<FMT, XT, 4, 2, 2, 2>(a, groups, s);
   else
     return choice == 0 ? launch_tiles_as<FMT, XT, 4, 1, 1, 4>(a, groups, s)
            : choice == 1 ? launch_tiles_as<FMT, XT, 4, 1, 2, 3>(a, groups, s)
@@ -452,24 +457,31 @@ int launch_tiles_of(const lin::Args& a, int64_t groups, int choice, hipStream_t 
 
 }  // namespace
 
-// The index of the tile.  One matrix: the least time by the table, rounds of workgroups on 256 units.  Groups,
-// of whose lengths the host knows only the mean: by that.  (The tests ask too: they have to run every tile.)
-extern "C" int bqm_internal_linear_choice(int x_type, int grouped, int64_t R, int64_t N, int64_t K, int64_t groups) {
-  const LinChoice* table = x_type == BQM_F32 ? kLinChoices32 : kLinChoices;
-  const int count = x_type == BQM_F32 ? 3 : 5;
+// The index of the tile.  One matrix: the least time by the table, in rounds of workgroups on 256 units and 4 us
+// for each.  Groups, of whose lengths the host knows only the mean, are short and long beside each other (their
+// short ends run as lower tiles): by the mean (128 experts of 1536 x 4096, Q4_0, skewed: 4 rows each 46 us with
+// the lowest tile and 54 with the widest, 32 rows 199, 167 with three row tiles and 171, 256 rows 1333, 786 and
+// 707), and lower where that leaves units without work.  (The tests ask too: they have to run every tile.)
+extern "C" int bqm_internal_linear_choice(int fmt, int x_type, int grouped, int64_t R, int64_t N, int64_t K, int64_t groups) {
+  const bool wide = x_type == BQM_F32;
+  const LinChoice* table = wide ? kLin32 : fmt == BQM_Q8_0 ? kLinQ8 : fmt == BQM_MXFP4 && x_type == BQM_BF16 ? kLinMx : kLinQ4;
+  auto workgroups = [&](int c) {
+    const int64_t bm = table[c].tm * 32, bn = table[c].tn * 128;
+    return (grouped ? groups + R / bm : (R + bm - 1) / bm) * ((N + bn - 1) / bn);
+  };
   if (grouped) {
     const int64_t mean = R / (groups > 0 ? groups : 1);
-    if (x_type == BQM_F32) return mean <= 16 ? 0 : (groups + R / 64) * ((N + 255) / 256) < 512 ? 1 : 2;
-    const int c = mean <= 6 ? 0 : mean <= 20 ? 1 : mean <= 96 ? 2 : 4;
-    return c == 4 && (groups + R / 128) * ((N + 255) / 256) < 512 ? 3 : c;
+    int c = wide ? mean > 16 : mean <= 6 ? 0 : mean < 24 ? 2 : 4;
+    while (c > 0 && workgroups(c) < 256) c--;
+    return c;
   }
   int best = 0;
   double least = 0;
-  for (int c = 0; c < count; c++) {
+  for (int c = 0; c < (wide ? kLinTiles32 : kLinTiles); c++) {
     const LinChoice& t = table[c];
-    const int64_t wgs = ((R + t.tm * 32 - 1) / (t.tm * 32)) * ((N + t.tn * 128 - 1) / (t.tn * 128)), round = 256 * t.resident;
-    const int64_t full = wgs / round, left = wgs % round;
-    const double step = full * t.step[t.resident - 1] + (left ? t.step[(left - 1) / 256] : 0.0f);
+    const int64_t wgs = workgroups(c), round = 256 * t.resident, full = wgs / round, left = wgs % round;
+    // (units that are done early start on the last round before the others end the one before)
+    const double step = full * t.step[t.resident - 1] + (left ? t.step[(left - 1) / 256] * (full ? 0.85f : 1.0f) : 0.0f);
     const double time = (double)((K + 63) / 64) * step + 4.0 * (full + (left > 0));
     if (c == 0 || time < least) best = c, least = time;
   }
@@ -477,7 +489,7 @@ extern "C" int bqm_internal_linear_choice(int x_type, int grouped, int64_t R, in
 }
 
 int launch_linear_tiles(int fmt, int x_type, const lin::Args& a, int64_t groups, hipStream_t s) {
-  const int c = bqm_internal_linear_choice(x_type, a.offsets != nullptr, a.R, a.N, (int64_t)a.nb * kQK, groups);
+  const int c = bqm_internal_linear_choice(fmt, x_type, a.offsets != nullptr, a.R, a.N, (int64_t)a.nb * kQK, groups);
 #define BQM_TILES(FMT)                                                      \
   return x_type == BQM_F32   ? launch_tiles_of<FMT, BQM_F32>(a, groups, c, s) \
          : x_type == BQM_F16 ? launch_tiles_of<FMT, BQM_F16>(a, groups, c, s) \

@@ -75,9 +75,10 @@ def tolerance(y, S, K, out, mul=None, res=None):
     few steps of 2^-23, the argument of exp in gelu_tanh is rounded five times and that of erfc twice, which counts
     against the value by |u| e^-|u| < 0.37 and t^2 e^-t^2 / sqrt(pi) < 0.21 of |z|: 16 steps of 2^-23 in all.  The product
     with mul and the sum with the residual round once each, relative to what they give; and half a step of out's type,
-    or of its smallest numbers."""
+    or of its smallest numbers.  Below 2^-126 fp32 has only the multiples of 2^-149, whatever the relative error: K
+    terms are added, each sum off by half of that at most, which mul scales."""
     m = 1.0 if mul is None else np.abs(mul)
-    err = (1.13 * 1.125 * _mxref.tolerance(K) + 16 * 2.0 ** -23) * S * m
+    err = (1.13 * 1.125 * _mxref.tolerance(K) + 16 * 2.0 ** -23) * S * m + K * 2.0 ** -150 * m
     mag = np.abs(y) + (0 if res is None else np.abs(res))
     f = torch.finfo(out)
     err = err + 2.0 ** -23 * mag
