@@ -260,6 +260,13 @@ struct RowTile {
   int e, rows;   // group; rows of the tile, 0: no such tile
   int64_t m0;    // the first of them
 };
+// Row tiles of `each` rows: exactly, or with groups at most, the whole ones and an end of each, no more than rows.
+inline int64_t most_tiles(bool grouped, int64_t R, int64_t groups, int64_t each) {
+  if (!grouped) return (R + each - 1) / each;
+  return groups + R / each < R ? groups + R / each : R;
+}
+inline int64_t most_tiles(const Args& a, int64_t groups, int64_t each) { return most_tiles(a.offsets != nullptr, a.R, groups, each); }
+
 // The row tiles of BM rows, as a workgroup of NT threads counts them (one barrier) and then finds one of them
 // (another): first the whole ones, groups ascending, then what is left of each group, so that the longest work
 // is given out first.  Offsets are kept within the rows, so that whatever they hold, no row outside is touched.
@@ -269,7 +276,7 @@ struct RowTiles {
   static constexpr int kWaves = NT / 64, kRoom = 2 * kWaves + 4;
   const Args& a;
   int (&room)[kRoom];
-  int e0, e1;              // the groups that this thread looks at
+  int e0, e1, lo0, hi0;    // the groups that this thread looks at; the rows of the first, often the only one
   int whole, parts;        // tiles of the groups before these
   int all_whole, all;
 
@@ -279,11 +286,11 @@ struct RowTiles {
   }
   template <typename F>
   __device__ __forceinline__ void each(F&& f) const {  // f(group, first row, rows) for those that have any
-    int lo = e0 < e1 ? at(e0) : 0;
-    for (int e = e0; e < e1; e++) {
-      const int hi = at(e + 1);
+    int lo = lo0, hi = hi0;
+    for (int e = e0; e < e1;) {
       if (hi > lo) f(e, lo, hi - lo);
       lo = hi;
+      if (++e < e1) hi = at(e + 1);
     }
   }
 
@@ -296,6 +303,8 @@ struct RowTiles {
     const int per = (a.E + NT - 1) / NT;
     e0 = tid * per < a.E ? tid * per : a.E;
     e1 = e0 + per < a.E ? e0 + per : a.E;
+    lo0 = hi0 = 0;
+    if (e0 < e1) lo0 = at(e0), hi0 = at(e0 + 1);
     int w = 0, p = 0;
     each([&](int, int, int rows) { w += rows / BM, p += rows % BM != 0; });
     whole = w, parts = p;
@@ -309,6 +318,7 @@ struct RowTiles {
     __syncthreads();
     whole -= w, parts -= p;
     all_whole = all = 0;
+#pragma unroll
     for (int k = 0; k < kWaves; k++) {
       const int u = __builtin_amdgcn_readfirstlane(room[k]), v = __builtin_amdgcn_readfirstlane(room[kWaves + k]);
       if (k < wave) whole += u, parts += v;

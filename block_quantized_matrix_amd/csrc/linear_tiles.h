@@ -2,9 +2,11 @@
 //
 // The matrix cores and the vector unit bind it together: a block of 32 x 32 outputs takes two
 // v_mfma_f32_32x32x16 (64 clocks of a SIMD) and 16 FMAs for the block's scale; the codes' conversion
-// comes on top, once for all the row tiles of a wave.  So a wave takes 64 weight rows by 128 rows (the
-// conversion of two tiles over eight products), and two waves share a SIMD, one's vector work under the
-// other's products.
+// (15 instructions for eight codes of Q4_0, 12 of Q8_0, 8 of MXFP4 to bf16) comes on top, once for all the row
+// tiles of a wave.  A SIMD issues one vector instruction in about 4.3 clocks, a wave alone one in 4.9 and a
+// matrix instruction takes some twelve of them, so the widest tile, 64 weight rows by 128 rows a wave, two waves
+// a SIMD, cannot pass 60 % of the matrix rate; it reaches 0.86 PFLOP/s (4096 x 17408 x 5120, Q4_0 and Q8_0, 850
+// us; fp16 0.92), with MXFP4's scales folded into the conversion 1.3 (562 us).
 #pragma once
 
 #include "linear.h"
@@ -15,9 +17,10 @@ namespace {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-// Four waves side by side along the weight rows (TN tiles of 32 each), all over the same TM tiles of 32 rows.
-// K advances by steps of two blocks.  The rows go from memory straight into LDS, four stages, three steps
-// ahead; codes and scales straight to the registers of the wave that converts them, D steps ahead.
+// NW waves side by side along the weight rows (TN tiles of 32 each), all over the same TM tiles of 32 rows.  K
+// advances by steps of two blocks.  The rows go from memory straight into LDS, four stages, some two steps
+// ahead; codes straight to the registers of the wave that converts them, one to two steps ahead; scales by way
+// of LDS of the wave's own, four steps at a time (asked for at every step they were a third of what L2 delivered).
 template <int FMT, int XT, int NW, int TN, int TM>
 struct LinTile {
   static constexpr int kWaves = NW, kBN = kWaves * TN * 32, kBM = TM * 32;
@@ -421,7 +424,7 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(OCC, OC
 template <int FMT, int XT, int NW, int TN, int TM, int OCC>
 int launch_tiles_as(const lin::Args& a, int64_t groups, hipStream_t s) {
   using C = LinTile<FMT, XT, NW, TN, TM>;
-  const int64_t tm = a.offsets ? groups + a.R / C::kBM : (a.R + C::kBM - 1) / C::kBM, tn = (a.N + C::kBN - 1) / C::kBN;
+  const int64_t tm = lin::most_tiles(a, groups, C::kBM), tn = (a.N + C::kBN - 1) / C::kBN;
   const int64_t grid = (a.offsets ? (tm + 7) / 8 * 8 : tm) * tn;
   if (grid > kMaxGrid) return BQM_E_SHAPE;
   hipLaunchKernelGGL((k_linear_tiles<FMT, XT, NW, TN, TM, OCC>), dim3((unsigned)grid), dim3(NW * 64), 0, s, a, (int)tm, (int)tn);
@@ -467,7 +470,7 @@ extern "C" int bqm_internal_linear_choice(int fmt, int x_type, int grouped, int6
   const LinChoice* table = wide ? kLin32 : fmt == BQM_Q8_0 ? kLinQ8 : fmt == BQM_MXFP4 && x_type == BQM_BF16 ? kLinMx : kLinQ4;
   auto workgroups = [&](int c) {
     const int64_t bm = table[c].tm * 32, bn = table[c].tn * 128;
-    return (grouped ? groups + R / bm : (R + bm - 1) / bm) * ((N + bn - 1) / bn);
+    return lin::most_tiles(grouped, R, groups, bm) * ((N + bn - 1) / bn);
   };
   if (grouped) {
     const int64_t mean = R / (groups > 0 ? groups : 1);
