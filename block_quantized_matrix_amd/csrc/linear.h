@@ -345,7 +345,10 @@ struct RowTiles {
     __syncthreads();
     const int e = __builtin_amdgcn_readfirstlane(room[2 * kWaves]);
     if (e < 0) return {0, 0, 0};
-    return {e, __builtin_amdgcn_readfirstlane(room[2 * kWaves + 2]), (int64_t)__builtin_amdgcn_readfirstlane(room[2 * kWaves + 1])};
+    // (offsets that fall and rise again over many rows can have more tiles than an int counts, and two groups the
+    // same number: the end of the rows holds for those too)
+    const int m0 = __builtin_amdgcn_readfirstlane(room[2 * kWaves + 1]), rows = __builtin_amdgcn_readfirstlane(room[2 * kWaves + 2]);
+    return {e, rows < (int)a.R - m0 ? rows : (int)a.R - m0, (int64_t)m0};
   }
 };
 

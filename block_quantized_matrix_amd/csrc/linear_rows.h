@@ -157,50 +157,51 @@ __global__ __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(OCC, OCC
 #pragma unroll
       for (int t = 0; t < T; t++) {
         if (t * 16 < (int)(r1 - r0)) {  // (loads go on: a branch around them would make the compiler wait for all)
-        // words (or pairs of them) of the four blocks to the lane groups, and each block's scale to all
-        uint32_t wop[4][4];
+          // words (or pairs of them) of the four blocks to the lane groups, and each block's scale to all
+          uint32_t wop[4][4];
 #pragma unroll
-        for (int l = 0; l < L; l++) {
-          u32x4 v = code[d][t][l];
-          mma::exchange<FMT != BQM_Q8_0>(v);
-          if constexpr (FMT == BQM_Q8_0) {
+          for (int l = 0; l < L; l++) {
+            u32x4 v = code[d][t][l];
+            mma::exchange<FMT != BQM_Q8_0>(v);
+            if constexpr (FMT == BQM_Q8_0) {
 #pragma unroll
-            for (int u = 0; u < 2; u++) {
-              uint32_t x0w[2], x1w[2];
-              bytes<XT>(v[2 * u], x0w);
-              bytes<XT>(v[2 * u + 1], x1w);
-              wop[2 * l + u][0] = x0w[0], wop[2 * l + u][1] = x0w[1], wop[2 * l + u][2] = x1w[0], wop[2 * l + u][3] = x1w[1];
-            }
-          } else {
+              for (int u = 0; u < 2; u++) {
+                uint32_t x0w[2], x1w[2];
+                bytes<XT>(v[2 * u], x0w);
+                bytes<XT>(v[2 * u + 1], x1w);
+                wop[2 * l + u][0] = x0w[0], wop[2 * l + u][1] = x0w[1], wop[2 * l + u][2] = x1w[0], wop[2 * l + u][3] = x1w[1];
+              }
+            } else {
 #pragma unroll
-            for (int u = 0; u < 4; u++) {
-              uint32_t lo[2], hi[2];
-              nibbles<FMT, XT>(v[u], lo, hi);
-              wop[u][0] = lo[0], wop[u][1] = lo[1], wop[u][2] = hi[0], wop[u][3] = hi[1];
+              for (int u = 0; u < 4; u++) {
+                uint32_t lo[2], hi[2];
+                nibbles<FMT, XT>(v[u], lo, hi);
+                wop[u][0] = lo[0], wop[u][1] = lo[1], wop[u][2] = hi[0], wop[u][3] = hi[1];
+              }
             }
           }
-        }
-        const uint32_t f = __float_as_uint(scale_from<FMT, XT>(scale[d][t]));
-        u32x4 fs{f, f, f, f};
-        mma::exchange<true>(fs);
+          const uint32_t f = __float_as_uint(scale_from<FMT, XT>(scale[d][t]));
+          u32x4 fs{f, f, f, f};
+          mma::exchange<true>(fs);
 #pragma unroll
-        for (int tm = 0; tm < TM; tm++)
-          if (TM == 1 || tm * 16 < at.rows)
+          for (int tm = 0; tm < TM; tm++)
+            if (TM == 1 || tm * 16 < at.rows) {
 #pragma unroll
-          for (int u = 0; u < 4; u++) {
-            const u32x4 w{wop[u][0], wop[u][1], wop[u][2], wop[u][3]};
-            f32x4 sum{};
+              for (int u = 0; u < 4; u++) {
+                const u32x4 w{wop[u][0], wop[u][1], wop[u][2], wop[u][3]};
+                f32x4 sum{};
 #pragma unroll
-            for (int p = 0; p < P; p++) {
-              const u32x4 x = xop[u][tm][p];
-              if constexpr (XT == BQM_F16)
-                sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, x), __builtin_bit_cast(f16x8, w), sum, 0, 0, 0);
-              else
-                sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, w), sum, 0, 0, 0);
+                for (int p = 0; p < P; p++) {
+                  const u32x4 x = xop[u][tm][p];
+                  if constexpr (XT == BQM_F16)
+                    sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, x), __builtin_bit_cast(f16x8, w), sum, 0, 0, 0);
+                  else
+                    sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, w), sum, 0, 0, 0);
+                }
+#pragma unroll
+                for (int r = 0; r < 4; r++) acc[t][tm][r] = fmaf(__uint_as_float(fs[u]), sum[r], acc[t][tm][r]);
+              }
             }
-#pragma unroll
-            for (int r = 0; r < 4; r++) acc[t][tm][r] = fmaf(__uint_as_float(fs[u]), sum[r], acc[t][tm][r]);
-          }
         }
         __builtin_amdgcn_sched_barrier(0);
         load_w(d, t, s + D * W);

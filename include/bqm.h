@@ -35,8 +35,9 @@
  *   - Sizes may be zero (nothing is launched, except that N > 0 with K = 0 writes
  *     zeros, the value of an empty sum).  K must be a multiple of 32.
  *   - Pointers passed to the products must be 16-byte aligned (torch allocations are).
- *   - Outputs must not alias inputs.  Results are deterministic: no atomic updates of
- *     data, a fixed summation order, the same bits on every run with the same launch.
+ *   - Outputs must not alias inputs (but for the linear layers' mul and residual).  Results are
+ *     deterministic: no atomic updates of data, a fixed summation order, the same bits on every run
+ *     with the same launch.
  *   - Host-side state, all safe to use from several threads: per device, the compute-unit
  *     count and the device address of qmv_id_sum_noalloc's array (cached once); per kernel,
  *     whether its static local memory fits (checked once); per workspace prepared by
@@ -62,16 +63,16 @@ typedef enum {
   BQM_E_NULL = 1,        /* a required pointer is NULL                          */
   BQM_E_SHAPE = 2,       /* negative size, K % 32 != 0, or a size over a limit  */
   BQM_E_ALIGN = 3,       /* a pointer is not 16-byte aligned                    */
-  BQM_E_UNSUPPORTED = 4, /* an unknown or refused format, type or score         */
+  BQM_E_UNSUPPORTED = 4, /* an unknown or refused format, type, score, activation */
   BQM_E_LAUNCH = 5       /* the HIP runtime refused a launch                    */
 } bqm_status;
 
-/* Block formats.  BQM_MXFP4 is taken by bqm_packed_bytes, bqm_repack and bqm_unpack, and has
- * products of its own (the *_mxfp4 calls); the calls with a fmt argument other than those three
- * refuse it with BQM_E_UNSUPPORTED. */
+/* Block formats.  BQM_MXFP4 is taken by bqm_packed_bytes, bqm_repack, bqm_unpack, bqm_embed, bqm_linear
+ * and bqm_linear_grouped, and has products of its own (the *_mxfp4 calls); the other calls with a fmt
+ * argument refuse it with BQM_E_UNSUPPORTED. */
 typedef enum { BQM_Q4_0 = 2, BQM_Q8_0 = 8, BQM_MXFP4 = 39 } bqm_fmt;
 
-/* Element types of float rows (router logits, the rows of the MXFP4 quantizer). */
+/* Element types of float rows (router logits, the rows of the MXFP4 quantizer and of the layers). */
 typedef enum { BQM_F32 = 0, BQM_F16 = 1, BQM_BF16 = 30 } bqm_type;
 
 /* Activations of bqm_linear and bqm_linear_grouped: z, max(z, 0), z / (1 + exp(-z)), z times the
@@ -374,7 +375,7 @@ int bqm_route(int score, int l_type, const void* logits, int64_t l_stride, const
  * computed in fp32 and rounded once to y_type.  fmt: any of the three.  w_packed: packed rows x K.  ids:
  * int32 [T]; a negative id gives a row of zeros, an id >= rows a row of NaN.  Y: [T][K] of y_type with
  * y_stride >= K elements from row to row, those between rows are left as they are.  MXFP4 weights beyond
- * fp32's largest number count as they are.  rows, T and K up to 2^30, y_stride too. */
+ * fp32's largest number count as they are, where |scale| is below 2^125.  rows, T and K up to 2^30, y_stride too. */
 int bqm_embed(int fmt, const void* w_packed, int64_t rows, int64_t K, const int32_t* ids, int64_t T, float scale,
               int y_type, void* Y, int64_t y_stride, hipStream_t stream);
 
@@ -384,13 +385,14 @@ int bqm_embed(int fmt, const void* w_packed, int64_t rows, int64_t K, const int3
  * fmt: any of the three.  X: [M][K] of x_type.  bias: fp32 [N] or NULL (0).  act: bqm_act.  mul, residual:
  * [M][N] of y_type, or NULL (1 and 0); mul makes a gated feed-forward's silu(gate) * up of the gate's
  * product.  Y: [M][N] of y_type; the elements between its rows are left as they are.  mul and residual
- * may be Y itself (same address and stride), each element is read before it is written.  Rows lie x_stride, mul_stride, res_stride
- * and y_stride elements apart, at least their length (a stride without a pointer is ignored); X's rows
- * have to start at multiples of 16 bytes, the others need not.
+ * may be Y itself (same address and stride): each element is read before it is written.  Rows lie x_stride,
+ * mul_stride, res_stride and y_stride elements apart, at least their length (a stride without a pointer is
+ * ignored); X's rows have to start at multiples of 16 bytes, the others need not, and a bias at one of 4.
  * Arithmetic: codes and rows meet as they are (fp32 rows in three bf16 parts, exact down to a resolution of
  * 2^-133), block scales in fp32, sums in fp32; one rounding to y_type at the end.  z meets the tolerance of
  * the products for inputs below 2^116 in magnitude (a block's sum without its scale has to stay a
- * number of fp32).  K = 0: the sum is 0.  K and x_stride up to BQM_LINEAR_MAX_K, the other strides up to 2^30. */
+ * number of fp32).  K = 0: the sum is 0.  K and x_stride up to BQM_LINEAR_MAX_K, the other strides up to 2^30;
+ * outputs that take 2^22 workgroups or more (of 144 columns by 4 rows at the least): BQM_E_SHAPE. */
 #define BQM_LINEAR_MAX_K (1 << 20)
 int bqm_linear(int fmt, const void* w_packed, int x_type, const void* X, int64_t x_stride, const float* bias, int act,
                const void* mul, int64_t mul_stride, const void* residual, int64_t res_stride, int y_type, void* Y,

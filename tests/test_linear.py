@@ -44,7 +44,8 @@ COMMON = [
     (dict(mul=GOOD, mul_stride=(1 << 30) + 1), SHAPE), (dict(res=GOOD, res_stride=(1 << 30) + 1), SHAPE),
     (dict(w=None), NULL), (dict(X=None), NULL), (dict(Y=None), NULL), (dict(w=ODD), ALIGN), (dict(X=ODD), ALIGN),
     (dict(Y=ODD), ALIGN), (dict(mul=ODD, mul_stride=8), ALIGN), (dict(res=ODD, res_stride=8), ALIGN), (dict(bias=ODD4), ALIGN),
-    (dict(x_stride=66), ALIGN), (dict(x_type=1, x_stride=68), ALIGN), (dict(N=0, Y=None, y_stride=0), OK)]
+    (dict(x_stride=66), ALIGN), (dict(x_type=1, x_stride=68), ALIGN), (dict(N=0, Y=None, y_stride=0), OK),
+    (dict(N=1 << 30, y_stride=1 << 30), SHAPE)]  # more workgroups than a launch holds
 
 
 @pytest.mark.parametrize("change,want", COMMON + [(dict(M=-1), SHAPE), (dict(M=(1 << 30) + 1), SHAPE), (dict(M=0, X=None, Y=None), OK)])
