@@ -3,8 +3,9 @@
 //
 // Bound by the bytes that it writes.  A wave takes runs of 512 numbers of a row, a lane eight on end of each: a
 // store of theirs covers whole lines, and the four lanes of a block read its scale and codes from one line.
-// The loads of its U runs go out together: each is a trip to memory behind that of the id (16384 x 5120 of
-// Q4_0 to bf16 with a run a wave: 76 us, with four 36; the output alone takes 25 at the rate of writes).
+// The loads of its U runs go out together: each is a trip to memory behind that of the id; and the many rows of
+// such calls are stored past the caches, which would hold them at the cost of writing back others (16384 x 5120
+// of Q4_0 to bf16, outputs in turn: a run a wave 77 us, four 56, stored past 41; a fill of the output takes 27).
 #pragma once
 
 #include "mxfp4.h"
@@ -84,7 +85,12 @@ __global__ __launch_bounds__(kEmbedWaves * 64) void k_embed(EmbedArgs a, typenam
         u32x4 v[sizeof(o) / 16];
         __builtin_memcpy(v, o, sizeof(o));
 #pragma unroll
-        for (int q = 0; q < (int)(sizeof(o) / 16); q++) reinterpret_cast<u32x4*>(y)[q] = v[q];
+        for (int q = 0; q < (int)(sizeof(o) / 16); q++) {
+          if (U > 1)
+            __builtin_nontemporal_store(v[q], reinterpret_cast<u32x4*>(y) + q);
+          else
+            reinterpret_cast<u32x4*>(y)[q] = v[q];
+        }
       } else {
 #pragma unroll
         for (int j = 0; j < 8; j++) y[j] = o[j];
