@@ -272,6 +272,31 @@ def test_embed_matches_definition(T, K, fmt, y_type):
         assert (whole[:, K:] == 9.0).all()
 
 
+@pytest.mark.parametrize("y_type", list(TYPES))
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("T,K", [(3300, 2592), (16500, 96)])
+def test_embed_many_rows(T, K, fmt, y_type):
+    """Calls large enough for several runs a wave, the last of a row short or absent."""
+    say("embed many", fmt, y_type, T, K)
+    n, out = 40, TYPES[y_type]
+    b = _linref.blocks(fmt, n, K, ("emb-m",))
+    wp = pack(fmt, b)
+    ids = torch.from_numpy(np.random.default_rng(T).integers(-2, n + 2, T).astype(np.int32)).to(DEV)
+    W = torch.from_numpy(_linref.dequantize(fmt, b)).to(DEV)
+    table = torch.cat([torch.zeros((2, K), dtype=torch.float64, device=DEV), W, torch.full((2, K), float("nan"), dtype=torch.float64, device=DEV)])
+    want = table[ids.long() + 2] * float(np.float32(0.1))
+    f = torch.finfo(out)  # the product in fp32, then the type: half a step each
+    most = want.abs() * (f.eps / 2 + 2.0 ** -24) * 1.01 + f.tiny * f.eps / 2
+    inside = (ids >= 0) & (ids < n)
+    for pad in (0, 3, 8):
+        whole = torch.full((T + 1, K + pad), 9.0, dtype=out, device=DEV)
+        bqm.bqm_embed(fmt, wp, n, K, ids, T, 0.1, whole, K + pad)
+        y = whole[:T, :K].double()
+        assert ((y - want).abs() <= most)[inside].all()
+        assert (y[ids < 0] == 0).all() and y[ids >= n].isnan().all()
+        assert (whole[:T, K:] == 9.0).all() and (whole[T] == 9.0).all()
+
+
 def test_embed_ids_outside():
     """Negative ids give zeros, ids past the table NaN; an empty table has no ids inside."""
     say("embed ids")
