@@ -233,9 +233,10 @@ __device__ __forceinline__ void lin_sums(const lin::Args& a, const lin::RowTile&
 #pragma unroll
     for (int t = 0; t < TN; t++) f[t] = g[t];
   };
-  // The Q-th step of four; whole steps, both blocks.
-  auto step = [&](auto qc, int s, const uint8_t* cur, const uint8_t* nxt, uint8_t* free) {
+  // The Q-th step of four; whole steps, both blocks.  TAIL: one of the last, behind the whole fours.
+  auto step = [&](auto qc, auto tail, int s, const uint8_t* cur, const uint8_t* nxt, uint8_t* free) {
     constexpr int Q = decltype(qc)::value, d = Q & 1;
+    constexpr bool TAIL = decltype(tail)::value;
     // codes: block 0 converts block 1 of this step, block 1 block 0 of the next
     if constexpr (L == 2) {
       load_codes(0, 2 * s + 2);
@@ -243,7 +244,7 @@ __device__ __forceinline__ void lin_sums(const lin::Args& a, const lin::RowTile&
     }
     block(std::integral_constant<int, 0>{}, s, L == 2 ? 1 : d, cur, cur, [] {});
     load_codes(L == 2 ? 1 : d, L == 2 ? 2 * s + 3 : s + 2);
-    if constexpr (Q == 0) load_scales((s >> 2) + 1);
+    if constexpr (Q == 0 && !TAIL) load_scales((s >> 2) + 1);
     if constexpr (Q == 3) {  // the next step's are asked for in the block that follows
       keep_scales((s >> 2) + 1);
       mx::wave_turn();
@@ -252,7 +253,8 @@ __device__ __forceinline__ void lin_sums(const lin::Args& a, const lin::RowTile&
     block(std::integral_constant<int, 1>{}, s, L == 2 ? 0 : d ^ 1, cur, nxt, [&] {
       // The rows of step s + 1 have arrived (after them came those of step s + 2, the codes of two blocks of
       // nibbles or four of bytes, and the scales of every fourth step), and every wave has read all of step s - 1.
-      vm_wait<PX + (L == 2 ? 4 : 2) * TN + (Q <= 1 ? (MX ? 4 : 1) : 0)>();
+      // A tail counts the rows of step s + 2 alone: the compiler leaves out what it loads for steps that never come.
+      vm_wait<TAIL ? PX : PX + (L == 2 ? 4 : 2) * TN + (Q <= 1 ? (MX ? 4 : 1) : 0)>();
       meet();
       load_x(s + 3, free);
       __builtin_amdgcn_sched_barrier(0);
@@ -278,14 +280,14 @@ __device__ __forceinline__ void lin_sums(const lin::Args& a, const lin::RowTile&
     __builtin_amdgcn_sched_barrier(0);
     int s = 0;  // (left in one place only: exits from each step had the sums copied, and spilled)
     for (; s + 4 <= whole; s += 4) {
-      step(std::integral_constant<int, 0>{}, s, lds0, lds1, lds3);
-      step(std::integral_constant<int, 1>{}, s + 1, lds1, lds2, lds0);
-      step(std::integral_constant<int, 2>{}, s + 2, lds2, lds3, lds1);
-      step(std::integral_constant<int, 3>{}, s + 3, lds3, lds0, lds2);
+      step(std::integral_constant<int, 0>{}, std::false_type{}, s, lds0, lds1, lds3);
+      step(std::integral_constant<int, 1>{}, std::false_type{}, s + 1, lds1, lds2, lds0);
+      step(std::integral_constant<int, 2>{}, std::false_type{}, s + 2, lds2, lds3, lds1);
+      step(std::integral_constant<int, 3>{}, std::false_type{}, s + 3, lds3, lds0, lds2);
     }
-    if (s < whole) step(std::integral_constant<int, 0>{}, s, lds0, lds1, lds3);
-    if (s + 1 < whole) step(std::integral_constant<int, 1>{}, s + 1, lds1, lds2, lds0);
-    if (s + 2 < whole) step(std::integral_constant<int, 2>{}, s + 2, lds2, lds3, lds1);
+    if (s < whole) step(std::integral_constant<int, 0>{}, std::true_type{}, s, lds0, lds1, lds3);
+    if (s + 1 < whole) step(std::integral_constant<int, 1>{}, std::true_type{}, s + 1, lds1, lds2, lds0);
+    if (s + 2 < whole) step(std::integral_constant<int, 2>{}, std::true_type{}, s + 2, lds2, lds3, lds1);
     if (nb & 1) {  // a last block without a partner, its codes already at hand
       const uint8_t* stage = (whole & 3) == 0 ? lds0 : (whole & 3) == 1 ? lds1 : (whole & 3) == 2 ? lds2 : lds3;
 #pragma unroll
