@@ -115,7 +115,7 @@ struct Args;  // linear.h
 int launch_linear(int fmt, const void* w, int E, const int32_t* offsets, int x_type, const void* X, int64_t x_stride,
                   const float* bias, int act, const void* mul, int64_t mul_stride, const void* res, int64_t res_stride,
                   int y_type, void* Y, int64_t y_stride, int64_t R, int64_t N, int64_t K, hipStream_t s);
-int launch_linear_rows(int fmt, int x_type, const lin::Args& a, int64_t groups, int64_t rows_each, hipStream_t s);
+int launch_linear_rows(int fmt, int x_type, const lin::Args& a, int64_t groups, hipStream_t s);
 int launch_linear_tiles(int fmt, int x_type, const lin::Args& a, int64_t groups, hipStream_t s);
 int launch_fill(float* y, int64_t n, float v, hipStream_t s);
 int cu_count();

@@ -230,10 +230,28 @@ __global__ __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(OCC, OCC
   }
 }
 
+// Rows of x that a workgroup takes, weight rows in eights, row tiles, runs of weight rows.
 struct RowsPlan {
   int rm, halves;
   int64_t tiles, span;
 };
+RowsPlan rows_plan(int x_type, bool grouped, int64_t R, int64_t N, int64_t groups) {
+  const int64_t each = (R + groups - 1) / groups;
+  RowsPlan p;
+  p.rm = each <= 4 ? 4 : each <= 16 || x_type == BQM_F32 ? 16 : 64;
+  p.tiles = lin::most_tiles(grouped, R, groups, p.rm);
+  const int64_t runs = (N + 7) / 8, most = p.rm == 64 ? 4 : 18;
+  const int64_t rounds = (runs * p.tiles + 256 * most - 1) / (256 * most);
+  p.halves = (int)((runs * p.tiles + 256 * rounds - 1) / (256 * rounds));
+  p.halves = p.halves > most ? (int)most : p.halves < runs ? p.halves : (int)runs;
+  p.span = (runs + p.halves - 1) / p.halves;
+  return p;
+}
+// Weight tiles of the kernel that takes a plan: the least that hold its run.
+constexpr int rows_kernel(int rm, int halves) {
+  const int T = (halves + 1) / 2;
+  return rm == 64 ? 2 : T <= 3 ? T : T <= 5 ? 5 : 9;
+}
 
 template <int FMT, int XT, int RM, int T>
 int launch_rows_as(const lin::Args& a, const RowsPlan& p, hipStream_t s) {
@@ -245,12 +263,12 @@ int launch_rows_as(const lin::Args& a, const RowsPlan& p, hipStream_t s) {
 }
 template <int FMT, int XT>
 int launch_rows_of(const lin::Args& a, const RowsPlan& p, hipStream_t s) {
-  const int T = (p.halves + 1) / 2;
+  const int T = rows_kernel(p.rm, p.halves);
 #define BQM_ROWS(RM)                                         \
-  return T <= 1   ? launch_rows_as<FMT, XT, RM, 1>(a, p, s)  \
-         : T <= 2 ? launch_rows_as<FMT, XT, RM, 2>(a, p, s)  \
-         : T <= 3 ? launch_rows_as<FMT, XT, RM, 3>(a, p, s)  \
-         : T <= 5 ? launch_rows_as<FMT, XT, RM, 5>(a, p, s)  \
+  return T == 1   ? launch_rows_as<FMT, XT, RM, 1>(a, p, s)  \
+         : T == 2 ? launch_rows_as<FMT, XT, RM, 2>(a, p, s)  \
+         : T == 3 ? launch_rows_as<FMT, XT, RM, 3>(a, p, s)  \
+         : T == 5 ? launch_rows_as<FMT, XT, RM, 5>(a, p, s)  \
                   : launch_rows_as<FMT, XT, RM, 9>(a, p, s)
   if (p.rm == 4) BQM_ROWS(4);
   if constexpr (XT != BQM_F32)
@@ -261,15 +279,8 @@ int launch_rows_of(const lin::Args& a, const RowsPlan& p, hipStream_t s) {
 
 }  // namespace
 
-int launch_linear_rows(int fmt, int x_type, const lin::Args& a, int64_t groups, int64_t rows_each, hipStream_t s) {
-  RowsPlan p;
-  p.rm = rows_each <= 4 ? 4 : rows_each <= 16 || x_type == BQM_F32 ? 16 : 64;
-  p.tiles = lin::most_tiles(a, groups, p.rm);
-  const int64_t runs = (a.N + 7) / 8, most = p.rm == 64 ? 4 : 18;
-  const int64_t rounds = (runs * p.tiles + 256 * most - 1) / (256 * most);
-  p.halves = (int)((runs * p.tiles + 256 * rounds - 1) / (256 * rounds));
-  p.halves = p.halves > most ? (int)most : p.halves < runs ? p.halves : (int)runs;
-  p.span = (runs + p.halves - 1) / p.halves;
+int launch_linear_rows(int fmt, int x_type, const lin::Args& a, int64_t groups, hipStream_t s) {
+  const RowsPlan p = rows_plan(x_type, a.offsets != nullptr, a.R, a.N, groups);
   if (p.tiles * p.span > kMaxGrid) return BQM_E_SHAPE;
 #define BQM_ROWS(FMT)                                                        \
   return x_type == BQM_F32   ? launch_rows_of<FMT, BQM_F32>(a, p, s)         \
@@ -292,6 +303,12 @@ extern "C" int bqm_internal_linear_rows(int x_type, int grouped, int64_t R, int6
   return lin::most_tiles(grouped, R, groups, each) * ((N + 31) / 32) <= (x_type == BQM_F32 ? 1024 : 256);
 }
 
+// The kernel's rows (times 16) and weight tiles, for the tests: they have to run every one.
+extern "C" int bqm_internal_linear_rows_kernel(int x_type, int grouped, int64_t R, int64_t N, int64_t groups) {
+  const RowsPlan p = rows_plan(x_type, grouped, R, N, groups);
+  return p.rm * 16 + rows_kernel(p.rm, p.halves);
+}
+
 int launch_linear(int fmt, const void* w, int E, const int32_t* offsets, int x_type, const void* X, int64_t x_stride,
                   const float* bias, int act, const void* mul, int64_t mul_stride, const void* res, int64_t res_stride,
                   int y_type, void* Y, int64_t y_stride, int64_t R, int64_t N, int64_t K, hipStream_t s) {
@@ -308,7 +325,7 @@ int launch_linear(int fmt, const void* w, int E, const int32_t* offsets, int x_t
   }
   const int64_t groups = offsets ? (E < R ? E : R) : 1;
   if (bqm_internal_linear_rows(x_type, offsets != nullptr, R, N, groups))
-    return launch_linear_rows(fmt, x_type, a, groups, (R + groups - 1) / groups, s);
+    return launch_linear_rows(fmt, x_type, a, groups, s);
   return launch_linear_tiles(fmt, x_type, a, groups, s);
 }
 
