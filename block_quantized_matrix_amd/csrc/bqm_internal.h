@@ -117,6 +117,7 @@ int launch_linear(int fmt, const void* w, int E, const int32_t* offsets, int x_t
                   int y_type, void* Y, int64_t y_stride, int64_t R, int64_t N, int64_t K, hipStream_t s);
 int launch_linear_rows(int fmt, int x_type, const lin::Args& a, int64_t groups, hipStream_t s);
 int launch_linear_tiles(int fmt, int x_type, const lin::Args& a, int64_t groups, hipStream_t s);
+int64_t linear_tiles_grid(int fmt, int x_type, bool grouped, int64_t R, int64_t N, int64_t K, int64_t groups);
 int launch_fill(float* y, int64_t n, float v, hipStream_t s);
 int cu_count();
 int launch_id_mma(int fmt, const void* w, const void* w_up, int E, int64_t N, int64_t K,

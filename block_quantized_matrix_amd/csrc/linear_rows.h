@@ -309,6 +309,13 @@ extern "C" int bqm_internal_linear_rows_kernel(int x_type, int grouped, int64_t 
   return p.rm * 16 + rows_kernel(p.rm, p.halves);
 }
 
+// Workgroups of a call, whichever the kernel: kMaxGrid at most are launched.
+extern "C" int64_t bqm_internal_linear_workgroups(int fmt, int x_type, int grouped, int64_t R, int64_t N, int64_t K, int64_t groups) {
+  if (!bqm_internal_linear_rows(x_type, grouped, R, N, groups)) return linear_tiles_grid(fmt, x_type, grouped, R, N, K, groups);
+  const RowsPlan p = rows_plan(x_type, grouped, R, N, groups);
+  return p.tiles * p.span;
+}
+
 int launch_linear(int fmt, const void* w, int E, const int32_t* offsets, int x_type, const void* X, int64_t x_stride,
                   const float* bias, int act, const void* mul, int64_t mul_stride, const void* res, int64_t res_stride,
                   int y_type, void* Y, int64_t y_stride, int64_t R, int64_t N, int64_t K, hipStream_t s) {

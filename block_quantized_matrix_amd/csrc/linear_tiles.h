@@ -423,11 +423,16 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(OCC, OC
     lin_core<FMT, XT, NW, TN, TM>(a, at, tn, lds0, lds1, lds2, lds3, scales);
 }
 
+// Workgroups of a call by tiles of bn weight rows and bm rows.
+int64_t lin_grid(bool grouped, int64_t R, int64_t N, int64_t groups, int64_t bn, int64_t bm) {
+  const int64_t tm = lin::most_tiles(grouped, R, groups, bm);
+  return (grouped ? (tm + 7) / 8 * 8 : tm) * ((N + bn - 1) / bn);
+}
 template <int FMT, int XT, int NW, int TN, int TM, int OCC>
 int launch_tiles_as(const lin::Args& a, int64_t groups, hipStream_t s) {
   using C = LinTile<FMT, XT, NW, TN, TM>;
   const int64_t tm = lin::most_tiles(a, groups, C::kBM), tn = (a.N + C::kBN - 1) / C::kBN;
-  const int64_t grid = (a.offsets ? (tm + 7) / 8 * 8 : tm) * tn;
+  const int64_t grid = lin_grid(a.offsets != nullptr, a.R, a.N, groups, C::kBN, C::kBM);
   if (grid > kMaxGrid) return BQM_E_SHAPE;
   hipLaunchKernelGGL((k_linear_tiles<FMT, XT, NW, TN, TM, OCC>), dim3((unsigned)grid), dim3(NW * 64), 0, s, a, (int)tm, (int)tn);
   return launch_status();
@@ -447,6 +452,10 @@ constexpr LinChoice kLinQ8[kLinTiles] = {{1, 1, 4, {0.68f, 0.98f, 1.28f, 1.32f}}
 constexpr LinChoice kLinMx[kLinTiles] = {{1, 1, 4, {0.38f, 0.43f, 0.55f, 0.60f}}, {1, 2, 3, {0.42f, 0.54f, 0.76f}}, {1, 3, 2, {0.50f, 0.67f}},
                                          {1, 4, 2, {0.57f, 0.83f}}, {2, 4, 2, {0.93f, 1.37f}}};
 constexpr LinChoice kLin32[kLinTiles32] = {{1, 1, 3, {0.92f, 1.35f, 1.85f}}, {2, 2, 2, {2.03f, 2.90f}}};
+
+const LinChoice* lin_table(int fmt, int x_type) {
+  return x_type == BQM_F32 ? kLin32 : fmt == BQM_Q8_0 ? kLinQ8 : fmt == BQM_MXFP4 && x_type == BQM_BF16 ? kLinMx : kLinQ4;
+}
 
 template <int FMT, int XT>
 int launch_tiles_of(const lin::Args& a, int64_t groups, int choice, hipStream_t s) {
@@ -469,7 +478,7 @@ int launch_tiles_of(const lin::Args& a, int64_t groups, int choice, hipStream_t 
 // 707), and lower where that leaves units without work.  (The tests ask too: they have to run every tile.)
 extern "C" int bqm_internal_linear_choice(int fmt, int x_type, int grouped, int64_t R, int64_t N, int64_t K, int64_t groups) {
   const bool wide = x_type == BQM_F32;
-  const LinChoice* table = wide ? kLin32 : fmt == BQM_Q8_0 ? kLinQ8 : fmt == BQM_MXFP4 && x_type == BQM_BF16 ? kLinMx : kLinQ4;
+  const LinChoice* table = lin_table(fmt, x_type);
   auto workgroups = [&](int c) {
     const int64_t bm = table[c].tm * 32, bn = table[c].tn * 128;
     return lin::most_tiles(grouped, R, groups, bm) * ((N + bn - 1) / bn);
@@ -491,6 +500,11 @@ extern "C" int bqm_internal_linear_choice(int fmt, int x_type, int grouped, int6
     if (c == 0 || time < least) best = c, least = time;
   }
   return best;
+}
+
+int64_t linear_tiles_grid(int fmt, int x_type, bool grouped, int64_t R, int64_t N, int64_t K, int64_t groups) {
+  const LinChoice& t = lin_table(fmt, x_type)[bqm_internal_linear_choice(fmt, x_type, grouped, R, N, K, groups)];
+  return lin_grid(grouped, R, N, groups, t.tn * 128, t.tm * 32);
 }
 
 int launch_linear_tiles(int fmt, int x_type, const lin::Args& a, int64_t groups, hipStream_t s) {

@@ -391,8 +391,9 @@ int bqm_embed(int fmt, const void* w_packed, int64_t rows, int64_t K, const int3
  * Arithmetic: codes and rows meet as they are (fp32 rows in three bf16 parts, exact down to a resolution of
  * 2^-133), block scales in fp32, sums in fp32; one rounding to y_type at the end.  z meets the tolerance of
  * the products for inputs below 2^116 in magnitude (a block's sum without its scale has to stay a
- * number of fp32).  K = 0: the sum is 0.  K and x_stride up to BQM_LINEAR_MAX_K, the other strides up to 2^30;
- * outputs that take 2^22 workgroups or more (of 144 columns by 4 rows at the least): BQM_E_SHAPE. */
+ * number of fp32).  K = 0: the sum is 0.  K and x_stride up to BQM_LINEAR_MAX_K, the other strides up to 2^30.
+ * Sizes with ceil(M / 32) * ceil(N / 128) < 2^22 are taken; above that a call may need more workgroups than a
+ * launch holds: BQM_E_SHAPE. */
 #define BQM_LINEAR_MAX_K (1 << 20)
 int bqm_linear(int fmt, const void* w_packed, int x_type, const void* X, int64_t x_stride, const float* bias, int act,
                const void* mul, int64_t mul_stride, const void* residual, int64_t res_stride, int y_type, void* Y,
@@ -407,7 +408,8 @@ int bqm_linear(int fmt, const void* w_packed, int x_type, const void* X, int64_t
  * [E + 1], device memory, not decreasing, from 0 or more up to R or less; rows of Y outside
  * offsets[0] .. offsets[E] are left as they are.  Offsets below 0 or above R count as 0 or R; where they
  * decrease, which rows of Y are written, and with what, is not defined (nothing outside Y's R rows is).
- * E <= BQM_QMV_ID_MAX_E; the rest as bqm_linear with M = R. */
+ * E <= BQM_QMV_ID_MAX_E.  Sizes with (min(E + R / 32, R) + 16) * ceil(N / 128) < 2^22 are taken: a group has row
+ * tiles of its own, however few its rows.  The rest as bqm_linear with M = R. */
 int bqm_linear_grouped(int fmt, const void* w_packed, int E, const int32_t* offsets, int x_type, const void* X,
                        int64_t x_stride, const float* bias, int act, const void* mul, int64_t mul_stride,
                        const void* residual, int64_t res_stride, int y_type, void* Y, int64_t y_stride, int64_t R,
