@@ -20,7 +20,8 @@ struct EmbedArgs {
   const int32_t* ids;
   int64_t scales_off, rows, K, ks, kg, units, y_stride;
   int per_row;  // units of a row
-  float scale;
+  float scale;  // the call's, times 2^-shift
+  int shift;    // 0 but beside MXFP4
   int vec;      // rows of Y start at multiples of 16 bytes
 };
 
@@ -62,10 +63,10 @@ __global__ __launch_bounds__(kEmbedWaves * 64) void k_embed(EmbedArgs a, typenam
           for (int h = 0; h < 2; h++) {
             const uint32_t v = code[r][h] >> (c & 2 ? 4 : 0);
             const float g[4] = {mx::pair_of<0>(v, 1.0f).x, mx::pair_of<1>(v, 1.0f).x, mx::pair_of<2>(v, 1.0f).x, mx::pair_of<3>(v, 1.0f).x};
-            // the block's scale last: a weight beyond fp32's largest number counts as it is
+            // the powers of two last: the product counts as it is where the weight or the scale alone is far from 1
 #pragma unroll
             for (int j = 0; j < 4; j++)
-              f[h * 4 + j] = bits[r] == mx::kNanScale ? __builtin_nanf("") : ldexpf(g[j] * a.scale, (int)bits[r] - 127);
+              f[h * 4 + j] = bits[r] == mx::kNanScale ? __builtin_nanf("") : ldexpf(g[j] * a.scale, (int)bits[r] - 127 + a.shift);
           }
         } else {
           const float d = (float)__builtin_bit_cast(_Float16, (uint16_t)bits[r]);
@@ -125,10 +126,11 @@ int launch_embed_of(const EmbedArgs& a, int64_t T, int type, void* Y, hipStream_
 
 int launch_embed(int fmt, const void* w, int64_t rows, int64_t K, const int32_t* ids, int64_t T, float scale, int y_type, void* Y,
                  int64_t y_stride, hipStream_t s) {
-  EmbedArgs a{static_cast<const uint8_t*>(w), ids, 0, rows, K, 0, 0, 0, y_stride, 0, scale, y_stride * (y_type == BQM_F32 ? 4 : 2) % 16 == 0};
+  EmbedArgs a{static_cast<const uint8_t*>(w), ids, 0, rows, K, 0, 0, 0, y_stride, 0, scale, 0, y_stride * (y_type == BQM_F32 ? 4 : 2) % 16 == 0};
   if (fmt == BQM_MXFP4) {
     const MxLayout L = mx_layout(rows, K);
     a.scales_off = L.scales_off, a.ks = L.ks, a.kg = L.kg;
+    if (__builtin_isfinite(scale)) a.scale = frexpf(scale, &a.shift);  // 0.5 to 1 in magnitude, or 0
     return launch_embed_of<BQM_MXFP4>(a, T, y_type, Y, s);
   }
   Layout L;

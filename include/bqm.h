@@ -374,8 +374,9 @@ int bqm_route(int score, int l_type, const void* logits, int64_t l_stride, const
  *     Y[t][k] = scale * dequant(W)[ids[t]][k]
  * computed in fp32 and rounded once to y_type.  fmt: any of the three.  w_packed: packed rows x K.  ids:
  * int32 [T]; a negative id gives a row of zeros, an id >= rows a row of NaN.  Y: [T][K] of y_type with
- * y_stride >= K elements from row to row, those between rows are left as they are.  MXFP4 weights beyond
- * fp32's largest number count as they are, where |scale| is below 2^125.  rows, T and K up to 2^30, y_stride too. */
+ * y_stride >= K elements from row to row, those between rows are left as they are.  Only the product has to be
+ * a number of fp32: an MXFP4 weight beyond its largest number and a scale below its smallest count as they
+ * are.  rows, T and K up to 2^30, y_stride too. */
 int bqm_embed(int fmt, const void* w_packed, int64_t rows, int64_t K, const int32_t* ids, int64_t T, float scale,
               int y_type, void* Y, int64_t y_stride, hipStream_t stream);
 
