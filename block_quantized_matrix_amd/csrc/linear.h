@@ -158,9 +158,24 @@ __device__ __forceinline__ void store_as(uint8_t* p, int64_t at, float v, int ty
 
 // z / (1 + 2^u).  The exponential and the reciprocal are the hardware's, each off by a step of fp32 at most, and
 // u's rounding counts |u| 2^-24 of the exponential: no more than a step of z where that counts.  (With expf and a
-// correctly rounded division the 512-token product of 17408 x 5120 takes 12 us longer.)
-__device__ __forceinline__ float over_one_plus_exp2(float z, float u) {
+// correctly rounded division the 512-token product of 17408 x 5120 takes 12 us longer.)  The reciprocal is 0 where
+// it would be below 2^-126: a far z has the exponential taken 64 powers of two lower, beside which 1 counts nothing.
+__device__ __forceinline__ float over_one_plus_exp2(float z, float u, bool far) {
+  if (far) return ldexpf(z * __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(u - 64.0f)), -64);
   return z * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(u));
+}
+// silu, or gelu's tanh form.  FAR: some z may be below -87 or -9.9, from where u is 125.5 or 122.7 and more.
+constexpr float kFarSilu = -87.0f, kFarTanh = -9.9f;
+template <bool FAR, int V>
+__device__ __forceinline__ void sigmoid_times(float (&z)[V], int act) {
+  if (act == BQM_ACT_SILU) {
+#pragma unroll
+    for (int j = 0; j < V; j++) z[j] = over_one_plus_exp2(z[j], z[j] * -1.44269504f, FAR && z[j] < kFarSilu);
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; j++)
+      z[j] = over_one_plus_exp2(z[j], -2.30220819f * (z[j] + 0.044715f * z[j] * z[j] * z[j]), FAR && z[j] < kFarTanh);
+  }
 }
 // The two gelus are written with the tail of their distribution, which keeps its digits far below 0.
 template <int V>
@@ -168,15 +183,17 @@ __device__ __forceinline__ void activate(float (&z)[V], int act) {
   if (act == BQM_ACT_RELU) {
 #pragma unroll
     for (int j = 0; j < V; j++) z[j] = z[j] < 0.0f ? 0.0f : z[j];  // a NaN stays
-  } else if (act == BQM_ACT_SILU) {
-#pragma unroll
-    for (int j = 0; j < V; j++) z[j] = over_one_plus_exp2(z[j], z[j] * -1.44269504f);
   } else if (act == BQM_ACT_GELU) {
 #pragma unroll
     for (int j = 0; j < V; j++) z[j] = 0.5f * z[j] * erfcf(z[j] * -0.70710678f);
-  } else if (act == BQM_ACT_GELU_TANH) {
+  } else if (act != BQM_ACT_NONE) {
+    float low = z[0];
 #pragma unroll
-    for (int j = 0; j < V; j++) z[j] = over_one_plus_exp2(z[j], -2.30220819f * (z[j] + 0.044715f * z[j] * z[j] * z[j]));
+    for (int j = 1; j < V; j++) low = fminf(low, z[j]);
+    if (__builtin_expect(low < (act == BQM_ACT_SILU ? kFarSilu : kFarTanh), 0))
+      sigmoid_times<true>(z, act);
+    else
+      sigmoid_times<false>(z, act);
   }
 }
 // y of row m (of all rows) and column n, whose group's bias starts at `bias`.
