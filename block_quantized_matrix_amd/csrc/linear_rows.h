@@ -7,7 +7,7 @@
 // rows' part of a step to the operands' order through LDS of its own, once for all its tiles, and its
 // codes from memory straight to registers, D steps ahead; nothing waits for another wave until the end,
 // where the waves' sums are added in order.  One row: 4096 x 4096 of Q4_0 6.1 us, 17408 x 5120 18.8, 34816 x 5120 of
-// Q8_0 45 (4.2 TB/s, of which some 8 us are its start and end); 5120 x 17408 of MXFP4 by 8 rows 20.1, from memory all.
+// Q8_0 45 (4.2 TB/s, of which some 8 us are its start and end); 5120 x 17408 of MXFP4 by 8 rows 20, from memory all.
 #pragma once
 
 #include "linear.h"
@@ -255,6 +255,9 @@ constexpr int rows_kernel(int rm, int halves) {
 
 template <int FMT, int XT, int RM, int T>
 int launch_rows_as(const lin::Args& a, const RowsPlan& p, hipStream_t s) {
+  // Sixteen waves where their registers allow: shorter walks of a long K (5120 x 17408 of MXFP4 by 8 rows 19.9 us, by
+  // eight waves 20.9); at K = 4096 and 5120 the longer sum at the end costs as much or more (4096 x 4096 of Q4_0 6.0
+  // and 5.7, eight experts of 1536 x 4096 11.6 and 10.6).
   constexpr int W = (XT != BQM_F32 && RM <= 16 && T <= 3) || (RM <= 4 && T <= 2) ? 16 : 8;
   constexpr int D = T == 1 ? 2 : 1;
   hipLaunchKernelGGL((k_linear_rows<FMT, XT, RM, T, D, W, W / 4>), dim3((unsigned)(p.tiles * p.span)), dim3(W * 64), 0, s, a, p.halves,
@@ -293,10 +296,12 @@ int launch_linear_rows(int fmt, int x_type, const lin::Args& a, int64_t groups, 
 }
 
 // Which of the two kernels: 1 for the one above.  Up to 16 rows it wins everywhere (17408 x 5120, Q4_0: 16 rows
-// 21.5 us, by tiles 40; 32 rows 63 and 40).  With more it does where its workgroups, which share K out among
+// 21.2 us, by tiles 40; 17 rows 43 and 38).  With more it does where its workgroups, which share K out among
 // their waves, are one round on 256 units (1024 x 4096: 512 rows 16 us, by tiles 29, 1024 rows 48 and 29;
-// 5120 x 17408, 64 rows 58 and 165); fp32 rows, of which it takes 16 at a time, up to four (4096 x 4096: 64 rows
-// 19 and 59, 256 rows 55 and 64).
+// 5120 x 17408, 64 rows 53 and 114); fp32 rows, of which it takes 16 at a time, up to four (4096 x 4096: 64 rows
+// 19 and 59, 256 rows 55 and 64).  The rule knows neither K nor a group's mean rows: with a long K the kernel above
+// would stay ahead for more rows (5120 x 17408, 65 rows 81 us, by tiles as chosen 114; 256 rows 132 and 135), and
+// for groups up to three tokens of eight experts in 128 (1536 x 4096, Q4_0: 3 tokens 25 and 30, 8 tokens 43 and 41).
 extern "C" int bqm_internal_linear_rows(int x_type, int grouped, int64_t R, int64_t N, int64_t groups) {
   if (R <= 16) return 1;
   const int64_t each = x_type == BQM_F32 ? 16 : 64;

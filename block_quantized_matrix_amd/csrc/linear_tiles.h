@@ -439,7 +439,10 @@ int launch_tiles_as(const lin::Args& a, int64_t groups, hipStream_t s) {
 }
 // The tiles: weight tiles and row tiles of 32 a wave, workgroups that a unit holds at most, and the time of a
 // step (us; 64 of K) where it holds one, two, ... of them, measured with N = 17408 and K = 5120, weights from
-// memory.  (fp32 rows take four times the LDS of the others' step, so their tiles are lower.)
+// memory.  (fp32 rows take four times the LDS of the others' step, so their tiles are lower.)  Q4_0's serve MXFP4 beside
+// fp16, whose scales are not folded, and one table fp32 rows of every format: the tile that they choose is within 8 % of
+// the best (17408 x 5120, MXFP4 beside fp16: 128 rows 59 us and 55, 512 rows 144 and 135, 4096 rows 794 and 764; fp32 rows:
+// 128 rows of Q8_0 167 and 160, 512 rows of each format the best).
 struct LinChoice {
   int tn, tm, resident;
   float step[4];
@@ -473,9 +476,14 @@ int launch_tiles_of(const lin::Args& a, int64_t groups, int choice, hipStream_t 
 
 // The index of the tile.  One matrix: the least time by the table, in rounds of workgroups on 256 units and 4 us
 // for each.  Groups, of whose lengths the host knows only the mean, are short and long beside each other (their
-// short ends run as lower tiles): by the mean (128 experts of 1536 x 4096, Q4_0, skewed: 4 rows each 46 us with
-// the lowest tile and 54 with the widest, 32 rows 199, 167 with three row tiles and 171, 256 rows 1333, 786 and
-// 707), and lower where that leaves units without work.  (The tests ask too: they have to run every tile.)
+// short ends run as lower tiles): by the mean, and lower where that leaves units without work.  128 experts of
+// 1536 x 4096, skewed, us with the lowest tile, with three row tiles and with the widest:
+//     mean    Q4_0             Q8_0             MXFP4
+//        4    67,  71,  82     106, 126, 123    44,  55,  49
+//       10    108, 93,  101    177, 141, 143    74,  70,  74
+//       32    193, 156, 169    303, 215, 202    121, 116, 109
+//      256                     -,   782, 683    -,   502, 412
+// (The tests ask too: they have to run every tile.)
 extern "C" int bqm_internal_linear_choice(int fmt, int x_type, int grouped, int64_t R, int64_t N, int64_t K, int64_t groups) {
   const bool wide = x_type == BQM_F32;
   const LinChoice* table = lin_table(fmt, x_type);
